@@ -345,6 +345,93 @@ int ds4sp_kv_row_bytes(int kv_format, int dims);
 ds4sp_status ds4sp_quantize_kv(const void* x, int rows, int dims, int kv_format, void* out,
                                void* stream);
 
+/* Types of the rows that ds4sp_rope, ds4sp_cache_write and ds4sp_cache_read take. */
+typedef enum { DS4SP_F16 = 0, DS4SP_BF16 = 1, DS4SP_F32 = 2 } ds4sp_dtype;
+
+/* Rotary positions. Of each head's values, [offset, offset + dims) are turned: pair i,
+ * (x[2i], x[2i+1]) in the interleaved layout and (x[i], x[i + dims/2]) in the halves one,
+ * counted from offset, becomes m * (a cos t - b sin t, a sin t + b cos t) with
+ * t = position * f_i. With f_i = base^(-2i/dims) unscaled:
+ *   scaling 0  none;
+ *           1  linear: f_i / factor;
+ *           2  NTK: base * factor^(dims / (dims - 2)) in place of base (dims >= 4);
+ *           3  YaRN: f_i / factor * r_i + f_i * (1 - r_i), with r_i = (i - low) / (high -
+ *              low) held to [0, 1], low = floor(c(beta_fast)), high = ceil(c(beta_slow)),
+ *              c(b) = dims * ln(orig_len / (2 pi b)) / (2 ln base), low and high held to
+ *              [0, dims - 1] and at least 0.001 apart.
+ * m is mscale where that is above 0; else 0.1 ln(factor) + 1 for YaRN with factor > 1, and
+ * 1 otherwise. Frequencies are computed in 64-bit floating point and angles kept as 64-bit
+ * fractions of a turn, so that far positions lose nothing. */
+typedef struct {
+    int dims;            /* values of a head that are turned: even, 2 .. 256 */
+    int offset;          /* the first of them */
+    int layout;          /* 0 = interleaved pairs, 1 = halves */
+    int scaling;         /* 0 none, 1 linear, 2 NTK, 3 YaRN */
+    double base;         /* > 1 */
+    double factor;       /* > 0 (scaling 1-3); ignored without scaling */
+    int orig_len;        /* >= 1 (scaling 3): the context the model was trained at */
+    double beta_fast;    /* scaling 3: turns over orig_len; <= 0 selects 32 */
+    double beta_slow;    /* likewise; <= 0 selects 1 */
+    double mscale;       /* <= 0 selects the scaling's own */
+} ds4sp_rope_config;
+
+/* Turn the rotary part of x [n_tokens, heads, head_dim] into out (the attention takes its
+ * queries and rows after rotation). Token and head strides are in values; the values of a
+ * head are contiguous, at the alignment of their type (16-byte aligned rows are faster).
+ * The head's other values are copied. out may be x with the same strides (in place);
+ * otherwise the two must not share elements, and out's heads must not overlap one another.
+ *   positions  [n_tokens] int32 (device), or NULL: row i is at pos0 + i * pos_step (raw
+ *              rows: the token and 1; compressed row j: 4 * j and 4)
+ *   transpose  1: the transposed rotation, the gradient of this function (its inverse
+ *              where m is 1)
+ * Computed in fp32, rounded once. Asynchronous on `stream`; argument errors are returned
+ * before the launch. The pointers belong to the current device. */
+ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype dtype, int n_tokens,
+                        int heads, int head_dim, long long x_token_stride, long long x_head_stride,
+                        void* out, long long out_token_stride, long long out_head_stride,
+                        const int32_t* positions, long long pos0, long long pos_step, int transpose,
+                        void* stream);
+
+/* Caches written as rows are produced. kv_format 0 .. 3 are those of ds4sp_config: fp16, Q8_0,
+ * Q4_0, "Q8 K / Q4 V", rows one after another. kv_format 5 holds e4m3 codes with one fp32
+ * scale 2^e for each block of 64 rows: value = code * 2^e, e the smallest integer with
+ * max|x| <= 448 * 2^e over the block's finite values, held to [-40, 40] (-40 for a block of
+ * zeros; larger values saturate, a NaN stays NaN), codes rounded half to even. Row j is
+ * stored at place j + j / 64 and block b's scale at the start of place 64 + 65 b, whose
+ * other bytes are zero; a place is `dims` bytes.
+ *
+ * ds4sp_cache_bytes: bytes of a cache of `rows` rows of `dims` values: kv_format 0 (a
+ * multiple of 8), 1 .. 3 (as for ds4sp_kv_row_bytes), 5 (a multiple of 16; whole blocks are
+ * counted); at most 4096 values, 0 for anything else.
+ *
+ * ds4sp_cache_write: store x [n, dims] (dtype, rows x_stride values apart) as rows row0 ..
+ * row0+n-1 of the cache of cache_rows rows. rope (may be NULL) turns part of each row first;
+ * the turned values are rounded only by the cache's format. positions, pos0 and pos_step as
+ * for ds4sp_rope. In kv_format 5 a write that starts inside a block (row0 % 64 != 0) appends
+ * to it: the rows before row0 must have been written (their scale is read); the block's
+ * scale becomes the larger of theirs and the new rows', and where it grows their codes are
+ * rounded again to it. Writing a row again (a rejected draft's place) is such an append. Rows
+ * after the last one written are left as they are, but in kv_format 5 rows of the same block
+ * lose their meaning, since the scale is the block's. Two writes to one block must not run at
+ * the same time.
+ *
+ * ds4sp_cache_read: rows `rows` [n] (int32, device; any order, repeats allowed), or row0 ..
+ * row0+n-1 where rows is NULL, as dtype values in out [n, dims] (out_stride values apart):
+ * code * scale in fp32, rounded once. part 0 is the key (all dims), 1 the value (the first
+ * 512; kv_format 3 stores it apart). An index outside [0, cache_rows) reads as zeros.
+ *
+ * Both are asynchronous on `stream`; argument errors are returned before the launch. The
+ * cache is 16-byte aligned; x and out need the alignment of their type (16-byte aligned rows
+ * are faster). The pointers belong to the current device. */
+size_t ds4sp_cache_bytes(int kv_format, int dims, long long rows);
+ds4sp_status ds4sp_cache_write(void* cache, int kv_format, int dims, int cache_rows, int row0, int n,
+                               const void* x, ds4sp_dtype dtype, long long x_stride,
+                               const ds4sp_rope_config* rope, const int32_t* positions, long long pos0,
+                               long long pos_step, void* stream);
+ds4sp_status ds4sp_cache_read(const void* cache, int kv_format, int dims, int cache_rows,
+                              const int32_t* rows, int row0, int n, int part, void* out,
+                              ds4sp_dtype dtype, long long out_stride, void* stream);
+
 /* Measurement helper, not a step of the path: the bandwidth ceiling of the attention
  * kernel's access pattern. Reads n rows of row_bytes (a multiple of 16, at most 1152)
  * from `table` [table_rows, row_bytes] at the row indices idx[0..n) (each in

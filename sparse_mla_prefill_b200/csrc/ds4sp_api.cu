@@ -21,7 +21,9 @@
 #include "indexer_tcgen05.cuh"
 #include "indexer_topk_fused.cuh"
 #include "indexer_pair.cuh"
+#include "kv_cache.cuh"
 #include "probe_gather.cuh"
+#include "rope.cuh"
 #include "sparse_attn_mma.cuh"
 #include "sparse_attn_tc.cuh"
 #include "topk_radix.cuh"
@@ -859,6 +861,145 @@ ds4sp_status prefill_range(ds4sp_handle* h, int t0, int n_q, const void* q, cons
     return sparse_attn_impl(h, qh, kv_raw, kv_cmp, tk, t0, n_q, ot, s, prefetch, prefetch_bytes);
 }
 
+// ---------------------------------------------------------------- rotary, cache rows
+
+int dtype_bytes(ds4sp_dtype t) { return t == DS4SP_F16 || t == DS4SP_BF16 ? 2 : t == DS4SP_F32 ? 4 : 0; }
+
+ds4sp_status check_elem_ptr(const void* p, int elem, const char* name) {
+    if (!p) return fail(DS4SP_ERR_INVALID_ARG, "%s is null", name);
+    if (reinterpret_cast<uintptr_t>(p) % elem) return fail(DS4SP_ERR_INVALID_ARG, "%s is not %d-byte aligned", name, elem);
+    return DS4SP_OK;
+}
+
+// The kernel's table for a rotary configuration: each pair's frequency in turns, as a
+// fraction of 2^64 (the frequency itself in 64-bit floating point).
+ds4sp_status rope_table(const ds4sp_rope_config* cfg, int transpose, RopeTable* tab) {
+    if (!cfg) return fail(DS4SP_ERR_INVALID_ARG, "rope configuration is null");
+    const ds4sp_rope_config& c = *cfg;
+    if (c.dims < 2 || c.dims > kRopeMaxDims || c.dims % 2 || c.offset < 0)
+        return fail(DS4SP_ERR_INVALID_ARG, "rotary dims %d at offset %d (even, 2 .. %d, offset >= 0)", c.dims,
+                    c.offset, kRopeMaxDims);
+    if (c.layout != 0 && c.layout != 1) return fail(DS4SP_ERR_INVALID_ARG, "rotary layout %d (0 or 1)", c.layout);
+    if (c.scaling < 0 || c.scaling > 3) return fail(DS4SP_ERR_INVALID_ARG, "rotary scaling %d (0 .. 3)", c.scaling);
+    if (!(c.base > 1.0) || !std::isfinite(c.base)) return fail(DS4SP_ERR_INVALID_ARG, "rotary base %g (> 1)", c.base);
+    if (c.scaling != 0 && (!(c.factor > 0.0) || !std::isfinite(c.factor)))
+        return fail(DS4SP_ERR_INVALID_ARG, "rotary factor %g (> 0)", c.factor);
+    if (c.scaling == 2 && c.dims < 4) return fail(DS4SP_ERR_INVALID_ARG, "NTK scaling needs 4 rotary dims");
+    if (c.scaling == 3 && c.orig_len < 1) return fail(DS4SP_ERR_INVALID_ARG, "YaRN orig_len %d (>= 1)", c.orig_len);
+    if (std::isnan(c.beta_fast) || std::isnan(c.beta_slow) || std::isnan(c.mscale) || std::isinf(c.mscale))
+        return fail(DS4SP_ERR_INVALID_ARG, "rotary beta_fast, beta_slow or mscale is not a number");
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    const double d = c.dims, s = c.scaling == 0 ? 1.0 : c.factor;
+    const double base = c.scaling == 2 ? c.base * std::pow(s, d / (d - 2.0)) : c.base;
+    double low = 0.0, high = 1.0;
+    if (c.scaling == 3) {
+        auto pair_of = [&](double turns) { return d * std::log(c.orig_len / (turns * kTwoPi)) / (2.0 * std::log(c.base)); };
+        const double fast = c.beta_fast > 0.0 ? c.beta_fast : 32.0, slow = c.beta_slow > 0.0 ? c.beta_slow : 1.0;
+        low = std::min(std::max(std::floor(pair_of(fast)), 0.0), d - 1.0);
+        high = std::min(std::max(std::ceil(pair_of(slow)), 0.0), d - 1.0);
+        if (high - low < 0.001) high = low + 0.001;
+    }
+    std::memset(tab, 0, sizeof(*tab));
+    for (int i = 0; i < c.dims / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / d);
+        if (c.scaling == 1) f /= s;
+        if (c.scaling == 3) {
+            const double r = std::min(std::max((i - low) / (high - low), 0.0), 1.0);
+            f = f / s * r + f * (1.0 - r);
+        }
+        // In turns, modulo one (a factor below 1/2pi makes a step of more than a turn):
+        // 32 bits at a time, since a 64-bit fraction does not fit a double's mantissa.
+        const double turns = f / kTwoPi, frac = turns - std::floor(turns);
+        const double top = std::floor(std::ldexp(frac, 32));
+        tab->step[i] = ((uint64_t)top << 32) + (uint64_t)std::ldexp(std::ldexp(frac, 32) - top, 32);
+    }
+    const double m = c.mscale > 0.0 ? c.mscale : c.scaling == 3 && s > 1.0 ? 0.1 * std::log(s) + 1.0 : 1.0;
+    tab->m = (float)m;
+    tab->dims = c.dims;
+    tab->offset = c.offset;
+    tab->half_layout = c.layout;
+    tab->transpose = transpose != 0;
+    return DS4SP_OK;
+}
+
+template <class T, int V>
+void launch_rope_v(RopeParams& p, cudaStream_t s) {
+    // Four heads a thread (cos and sin computed once for them) where that leaves every SM
+    // its threads; one head a thread for small calls, where latency counts.
+    const long long chunks = (long long)p.n * p.per_head;
+    const bool many = p.heads >= 4 && chunks * ((p.heads + 3) / 4) >= 148LL * 1024;
+    p.groups = many ? (p.heads + 3) / 4 : p.heads;
+    const unsigned grid = (unsigned)((chunks * p.groups + 255) / 256);
+    if (many)
+        rope_kernel<T, V, 4><<<grid, 256, 0, s>>>(p);
+    else
+        rope_kernel<T, V, 1><<<grid, 256, 0, s>>>(p);
+}
+
+void launch_rope(RopeParams& p, ds4sp_dtype t, int v, cudaStream_t s) {
+    if (t == DS4SP_F32) {
+        if (v == 4) launch_rope_v<float, 4>(p, s);
+        else if (v == 2) launch_rope_v<float, 2>(p, s);
+        else launch_rope_v<float, 1>(p, s);
+    } else if (t == DS4SP_BF16) {
+        if (v == 8) launch_rope_v<__nv_bfloat16, 8>(p, s);
+        else if (v == 2) launch_rope_v<__nv_bfloat16, 2>(p, s);
+        else launch_rope_v<__nv_bfloat16, 1>(p, s);
+    } else {
+        if (v == 8) launch_rope_v<__half, 8>(p, s);
+        else if (v == 2) launch_rope_v<__half, 2>(p, s);
+        else launch_rope_v<__half, 1>(p, s);
+    }
+}
+
+// Bytes of a stored row (kv_format 5: of a place), 0 for a format or width that has none.
+int cache_row_bytes(int kv_format, int dims) {
+    if (kv_format == kFmtF16) return dims >= 8 && dims % 8 == 0 && dims <= 4096 ? 2 * dims : 0;
+    if (kv_format == kFmtE4M3) return dims >= 16 && dims % 16 == 0 && dims <= 4096 ? dims : 0;
+    return ds4sp_kv_row_bytes(kv_format, dims);
+}
+
+template <class T>
+void launch_cache_write_t(const CacheRows& p, const RopeTable& tab, uint8_t* cache, int fmt, int rb, cudaStream_t s) {
+    const unsigned grid = (unsigned)(((long long)p.n * (p.dims / 8) + 255) / 256);
+    const unsigned blocks = (unsigned)((p.row0 % kScaleBlock + (long long)p.n + kScaleBlock - 1) / kScaleBlock);
+    switch (fmt) {
+        case kFmtF16: cache_write_kernel<T, kFmtF16><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
+        case kFmtQ8: cache_write_kernel<T, kFmtQ8><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
+        case kFmtQ4: cache_write_kernel<T, kFmtQ4><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
+        case kFmtQ8Q4: cache_write_kernel<T, kFmtQ8Q4><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
+        default:
+            if (p.dims <= 64 * kE4M3Held)
+                cache_write_e4m3_kernel<T, true><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
+            else
+                cache_write_e4m3_kernel<T, false><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
+    }
+}
+
+void launch_cache_write(const CacheRows& p, const RopeTable& tab, uint8_t* cache, int fmt, int rb, ds4sp_dtype t,
+                        cudaStream_t s) {
+    if (t == DS4SP_F32) launch_cache_write_t<float>(p, tab, cache, fmt, rb, s);
+    else if (t == DS4SP_BF16) launch_cache_write_t<__nv_bfloat16>(p, tab, cache, fmt, rb, s);
+    else launch_cache_write_t<__half>(p, tab, cache, fmt, rb, s);
+}
+
+template <class T>
+void launch_cache_read_t(const CacheRead& p, int fmt, T* out, cudaStream_t s) {
+    const unsigned grid = (unsigned)(((long long)p.n * (p.out_dims / 8) + 255) / 256);
+    switch (fmt) {
+        case kFmtF16: cache_read_kernel<T, kFmtF16><<<grid, 256, 0, s>>>(p, out); break;
+        case kFmtQ8: cache_read_kernel<T, kFmtQ8><<<grid, 256, 0, s>>>(p, out); break;
+        case kFmtQ4: cache_read_kernel<T, kFmtQ4><<<grid, 256, 0, s>>>(p, out); break;
+        default: cache_read_kernel<T, kFmtE4M3><<<grid, 256, 0, s>>>(p, out);
+    }
+}
+
+void launch_cache_read(const CacheRead& p, int fmt, void* out, ds4sp_dtype t, cudaStream_t s) {
+    if (t == DS4SP_F32) launch_cache_read_t(p, fmt, static_cast<float*>(out), s);
+    else if (t == DS4SP_BF16) launch_cache_read_t(p, fmt, static_cast<__nv_bfloat16*>(out), s);
+    else launch_cache_read_t(p, fmt, static_cast<__half*>(out), s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1294,6 +1435,156 @@ ds4sp_status ds4sp_quantize_kv(const void* x, int rows, int dims, int kv_format,
         if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
     }
     return DS4SP_OK;
+}
+
+ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype dtype, int n_tokens,
+                        int heads, int head_dim, long long x_token_stride, long long x_head_stride,
+                        void* out, long long out_token_stride, long long out_head_stride,
+                        const int32_t* positions, long long pos0, long long pos_step, int transpose,
+                        void* stream) {
+    const TraceRange trace("ds4sp_rope");
+    RopeParams p;
+    DS4SP_TRY(rope_table(cfg, transpose, &p.tab));
+    const int es = dtype_bytes(dtype);
+    if (es == 0) return fail(DS4SP_ERR_INVALID_ARG, "dtype %d", (int)dtype);
+    if (n_tokens < 0 || heads < 1 || head_dim < 1)
+        return fail(DS4SP_ERR_INVALID_ARG, "n_tokens %d, heads %d, head_dim %d", n_tokens, heads, head_dim);
+    if ((long long)cfg->offset + cfg->dims > head_dim)
+        return fail(DS4SP_ERR_INVALID_ARG, "rotary dims [%d, %d) of a head of %d", cfg->offset,
+                    cfg->offset + cfg->dims, head_dim);
+    if (x_token_stride < 0 || x_head_stride < 0 || (n_tokens > 1 && out_token_stride < head_dim) ||
+        (heads > 1 && out_head_stride < head_dim))
+        return fail(DS4SP_ERR_INVALID_ARG, "strides of x (%lld, %lld) and out (%lld, %lld)", x_token_stride,
+                    x_head_stride, out_token_stride, out_head_stride);
+    if (n_tokens == 0) return DS4SP_OK;
+    DS4SP_TRY(check_elem_ptr(x, es, "x"));
+    DS4SP_TRY(check_elem_ptr(out, es, "out"));
+    if (reinterpret_cast<uintptr_t>(positions) & 3u)
+        return fail(DS4SP_ERR_INVALID_ARG, "positions is not 4-byte aligned");
+    p.x = x;
+    p.out = out;
+    p.positions = positions;
+    p.x_ts = x_token_stride;
+    p.x_hs = x_head_stride;
+    p.o_ts = out_token_stride;
+    p.o_hs = out_head_stride;
+    p.pos0 = pos0;
+    p.pos_step = pos_step;
+    p.n = n_tokens;
+    p.heads = heads;
+    // The widest access that every address and chunk boundary allows: 16 bytes, two values
+    // or one.
+    const int half = p.tab.half_layout ? cfg->dims / 2 : cfg->dims;
+    auto whole = [&](int v) {
+        const bool strided = n_tokens == 1 || (x_token_stride % v == 0 && out_token_stride % v == 0);
+        const bool headed = heads == 1 || (x_head_stride % v == 0 && out_head_stride % v == 0);
+        return strided && headed && half % v == 0 && cfg->offset % v == 0 && head_dim % v == 0 &&
+               reinterpret_cast<uintptr_t>(x) % (v * es) == 0 && reinterpret_cast<uintptr_t>(out) % (v * es) == 0;
+    };
+    const int v = whole(16 / es) ? 16 / es : whole(2) ? 2 : 1;
+    const bool in_place = x == out && x_token_stride == out_token_stride && x_head_stride == out_head_stride;
+    p.rot = p.tab.half_layout ? half / v : cfg->dims / (v < 2 ? 2 : v);
+    p.per_head = p.rot + (in_place ? 0 : (head_dim - cfg->dims) / v);
+    if ((double)n_tokens * heads * p.per_head > 256.0 * 0x7fffffff)
+        return fail(DS4SP_ERR_INVALID_ARG, "%d tokens of %d heads is too many", n_tokens, heads);
+    launch_rope(p, dtype, v, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DS4SP_OK : cuda_fail(e, "rope launch");
+}
+
+size_t ds4sp_cache_bytes(int kv_format, int dims, long long rows) {
+    if (rows < 0 || rows > (1LL << 31) - 1) return 0;
+    const int rb = cache_row_bytes(kv_format, dims);
+    if (rb == 0) return 0;
+    if (kv_format != kFmtE4M3) return (size_t)rows * rb;
+    return (size_t)((rows + kScaleBlock - 1) / kScaleBlock) * (kScaleBlock + 1) * rb;
+}
+
+ds4sp_status ds4sp_cache_write(void* cache, int kv_format, int dims, int cache_rows, int row0, int n,
+                               const void* x, ds4sp_dtype dtype, long long x_stride,
+                               const ds4sp_rope_config* rope, const int32_t* positions, long long pos0,
+                               long long pos_step, void* stream) {
+    const TraceRange trace("ds4sp_cache_write");
+    const int rb = cache_row_bytes(kv_format, dims);
+    if (rb == 0) return fail(DS4SP_ERR_INVALID_ARG, "kv_format %d with rows of %d values", kv_format, dims);
+    const int es = dtype_bytes(dtype);
+    if (es == 0) return fail(DS4SP_ERR_INVALID_ARG, "dtype %d", (int)dtype);
+    if (n < 0 || row0 < 0 || (long long)row0 + n > cache_rows)
+        return fail(DS4SP_ERR_INVALID_ARG, "rows [%d, %lld) of a cache of %d", row0, (long long)row0 + n, cache_rows);
+    if (x_stride < 0) return fail(DS4SP_ERR_INVALID_ARG, "x_stride %lld", x_stride);
+    RopeTable tab;
+    std::memset(&tab, 0, sizeof(tab));
+    if (rope) {
+        DS4SP_TRY(rope_table(rope, 0, &tab));
+        if ((long long)rope->offset + rope->dims > dims)
+            return fail(DS4SP_ERR_INVALID_ARG, "rotary dims [%d, %d) of rows of %d", rope->offset,
+                        rope->offset + rope->dims, dims);
+    }
+    if (n == 0) return DS4SP_OK;
+    DS4SP_TRY(check_ptr(cache, "cache"));
+    DS4SP_TRY(check_elem_ptr(x, es, "x"));
+    if (reinterpret_cast<uintptr_t>(positions) & 3u)
+        return fail(DS4SP_ERR_INVALID_ARG, "positions is not 4-byte aligned");
+    CacheRows p;
+    p.x = x;
+    p.x_ld = x_stride;
+    p.positions = positions;
+    p.pos0 = pos0;
+    p.pos_step = pos_step;
+    p.n = n;
+    p.row0 = row0;
+    p.dims = dims;
+    p.rotate = rope != nullptr;
+    const int part = !rope ? 8 : tab.half_layout ? tab.dims / 2 : tab.dims;
+    p.fast = aligned16(x) && (n == 1 || x_stride * es % 16 == 0) && part % 8 == 0 && tab.offset % 8 == 0;
+    if ((long long)n * (dims / 8) / 256 + 1 > 0x7fffffffLL) return fail(DS4SP_ERR_INVALID_ARG, "%d rows is too many", n);
+    launch_cache_write(p, tab, static_cast<uint8_t*>(cache), kv_format, rb, dtype, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DS4SP_OK : cuda_fail(e, "cache write launch");
+}
+
+ds4sp_status ds4sp_cache_read(const void* cache, int kv_format, int dims, int cache_rows,
+                              const int32_t* rows, int row0, int n, int part, void* out,
+                              ds4sp_dtype dtype, long long out_stride, void* stream) {
+    const TraceRange trace("ds4sp_cache_read");
+    const int rb = cache_row_bytes(kv_format, dims);
+    if (rb == 0) return fail(DS4SP_ERR_INVALID_ARG, "kv_format %d with rows of %d values", kv_format, dims);
+    const int es = dtype_bytes(dtype);
+    if (es == 0) return fail(DS4SP_ERR_INVALID_ARG, "dtype %d", (int)dtype);
+    if (part != 0 && part != 1) return fail(DS4SP_ERR_INVALID_ARG, "part %d (0 = key, 1 = value)", part);
+    if (part == 1 && dims < kValueDims)
+        return fail(DS4SP_ERR_INVALID_ARG, "a value part of %d in rows of %d", kValueDims, dims);
+    if (cache_rows < 0 || n < 0 || (!rows && (row0 < 0 || (long long)row0 + n > cache_rows)))
+        return fail(DS4SP_ERR_INVALID_ARG, "rows [%d, %lld) of a cache of %d", row0, (long long)row0 + n, cache_rows);
+    const int out_dims = part == 1 ? kValueDims : dims;
+    if (n > 1 && out_stride < out_dims) return fail(DS4SP_ERR_INVALID_ARG, "out_stride %lld", out_stride);
+    if (n == 0) return DS4SP_OK;
+    DS4SP_TRY(check_ptr(cache, "cache"));
+    DS4SP_TRY(check_elem_ptr(out, es, "out"));
+    if (reinterpret_cast<uintptr_t>(rows) & 3u) return fail(DS4SP_ERR_INVALID_ARG, "rows is not 4-byte aligned");
+    CacheRead p;
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.rows = rows;
+    p.row0 = row0;
+    p.n = n;
+    p.cache_rows = cache_rows;
+    p.dims = dims;
+    p.out_dims = out_dims;
+    p.row_bytes = rb;
+    p.part_off = 0;
+    p.out_ld = out_stride;
+    p.fast = aligned16(out) && (n == 1 || out_stride * es % 16 == 0);
+    int fmt = kv_format;
+    if (fmt == kFmtQ8Q4) {
+        fmt = part == 1 ? kFmtQ4 : kFmtQ8;
+        if (part == 1) {
+            p.part_off = quant_row_bytes(kFmtQ8, dims);
+            p.dims = kValueDims;
+        }
+    }
+    launch_cache_read(p, fmt, out, dtype, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DS4SP_OK : cuda_fail(e, "cache read launch");
 }
 
 ds4sp_status ds4sp_probe_gather(const void* table, int table_rows, int row_bytes,

@@ -1,0 +1,399 @@
+// Writing latent rows to a cache as they are produced, and reading them back.
+//
+// A row of x (fp16, bf16 or fp32) is rotated (optionally, the rotary part of the row:
+// rope.cuh's arithmetic, kept in fp32) and stored in the cache's format: fp16, the block
+// formats of quant_kv.cuh, or kv_format 5, whose rows the scaled attention reads:
+//
+//   e4m3 codes with one scale 2^e for each block of 64 rows; value = code * 2^e.
+//   e is the smallest integer with max|x| <= 448 * 2^e over the block's finite values,
+//   within [-40, 40] (all zero: -40); larger values, infinities among them, saturate at
+//   +-448 * 2^e, and a NaN stays one. A power of two costs a floating code no precision
+//   (only the smallest values lose range) and makes every stored value an exact product.
+//   The rows of block b are stored at places 65b .. 65b+63, and place 65b+64 is the
+//   block's record: its scale as fp32, then zeros. Places are `dims` bytes.
+//
+// A write that starts inside a block keeps the rows before it: the block's scale becomes
+// the larger of its own and the new rows', and if it grew the earlier codes are rounded
+// again to it. Rows after the written ones are left as they are.
+//
+// Bound: memory. Writing reads x once and stores codes; a CTA holds its block's rows in
+// registers between the maximum and the rounding.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "quant_kv.cuh"
+#include "rope.cuh"
+
+namespace ds4sp {
+
+constexpr int kFmtE4M3 = 5;
+constexpr int kScaleBlock = 64;                 // rows that share a scale
+constexpr int kScaleExpMax = 40;
+constexpr float kE4M3Max = 448.f;
+
+__host__ __device__ constexpr long long e4m3_place(long long row) { return row + row / kScaleBlock; }
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// The smallest e with top <= 448 * 2^e, in [-40, 40]. top is finite and >= 0.
+__device__ __forceinline__ int scale_exponent(float top) {
+    if (top == 0.f) return -kScaleExpMax;
+    // top < 2^(x+1) with x its exponent; 448 = 1.75 * 2^8
+    int e = max((int)(__float_as_uint(top) >> 23) - 127, -126) - 8;
+    e = min(max(e, -kScaleExpMax), kScaleExpMax);
+    if (top > kE4M3Max * pow2f(e)) ++e;
+    return min(e, kScaleExpMax);
+}
+
+struct CacheRows {                              // the rows a write takes
+    const void* x;
+    long long x_ld;                             // in values
+    const int32_t* positions;                   // NULL: pos0 + i * pos_step
+    long long pos0, pos_step;
+    int n, row0, dims;
+    int rotate;                                 // apply the table
+    int fast;                                   // x's rows are 16-byte aligned, and no chunk of
+                                                // eight is partly rotated
+};
+
+// Eight values of row i (of the n written) at dims 8c .. 8c+7, rotated, in fp32.
+template <class T>
+__device__ __forceinline__ void load_chunk(const CacheRows& p, const RopeTable& tab, const uint64_t* step,
+                                           int i, int c, float (&v)[8]) {
+    const T* row = static_cast<const T*>(p.x) + i * p.x_ld;
+    const int d0 = 8 * c;
+    if (p.fast) {
+        union { uint4 q[sizeof(T) / 2]; T e[8]; } a, b;
+#pragma unroll
+        for (int w = 0; w < (int)sizeof(T) / 2; ++w) a.q[w] = __ldg(reinterpret_cast<const uint4*>(row + d0) + w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = to_f32(a.e[k]);
+        if (!p.rotate || d0 < tab.offset || d0 >= tab.offset + tab.dims) return;
+        const long long pos = p.positions ? (long long)__ldg(p.positions + i) : p.pos0 + i * p.pos_step;
+        const int r0 = d0 - tab.offset, half = tab.dims / 2;
+        if (tab.half_layout) {
+            const bool upper = r0 >= half;
+            const T* other = row + (upper ? d0 - half : d0 + half);
+#pragma unroll
+            for (int w = 0; w < (int)sizeof(T) / 2; ++w) b.q[w] = __ldg(reinterpret_cast<const uint4*>(other) + w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 cs = rope_turn(step[(upper ? r0 - half : r0) + k], pos, tab.m);
+                const float o = to_f32(b.e[k]);
+                v[k] = upper ? o * cs.y + v[k] * cs.x : v[k] * cs.x - o * cs.y;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 cs = rope_turn(step[r0 / 2 + k], pos, tab.m);
+                const float a0 = v[2 * k], b0 = v[2 * k + 1];
+                v[2 * k] = a0 * cs.x - b0 * cs.y;
+                v[2 * k + 1] = a0 * cs.y + b0 * cs.x;
+            }
+        }
+        return;
+    }
+    const long long pos = !p.rotate ? 0 : p.positions ? (long long)p.positions[i] : p.pos0 + i * p.pos_step;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int d = d0 + k, r = d - tab.offset, half = tab.dims / 2;
+        v[k] = to_f32(row[d]);
+        if (!p.rotate || r < 0 || r >= tab.dims) continue;
+        const bool second = tab.half_layout ? r >= half : r & 1;
+        const int pair = tab.half_layout ? (second ? r - half : r) : r / 2;
+        const int od = tab.half_layout ? (second ? d - half : d + half) : (second ? d - 1 : d + 1);
+        const float2 cs = rope_turn(step[pair], pos, tab.m);
+        const float o = to_f32(row[od]);
+        v[k] = second ? o * cs.y + v[k] * cs.x : v[k] * cs.x - o * cs.y;
+    }
+}
+
+__device__ __forceinline__ void load_steps(const RopeTable& tab, int rotate, uint64_t* step) {
+    if (rotate)
+        for (int i = threadIdx.x; i < tab.dims / 2; i += blockDim.x) step[i] = tab.step[i];
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- fp16, Q8_0, Q4_0, Q8 K / Q4 V
+
+// The code bytes of eight values of a Q8_0 block of scale d.
+__device__ __forceinline__ uint2 q8_codes(const float (&v)[8], float d) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float q = d == 0.f ? 0.f : fminf(fmaxf(rintf(v[k] / d), -127.f), 127.f);
+        w[k / 4] |= (uint32_t)(uint8_t)(int8_t)(int)q << (8 * (k % 4));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// The codes of eight values of a Q4_0 block of scale d, one per byte.
+__device__ __forceinline__ uint2 q4_codes(const float (&v)[8], float d) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t n = d == 0.f ? 8u : (uint32_t)(int)fminf(fmaxf(rintf(v[k] / d) + 8.f, 0.f), 15.f);
+        w[k / 4] |= n << (8 * (k % 4));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Four lanes per block of 32 values, eight values each: the block's largest magnitude (and
+// for Q4_0 its first extreme) over the four by shuffles, the codes as in quantize_rows_kernel.
+// Rows are stored at out + row * row_bytes. FMT: kFmtF16, kFmtQ8, kFmtQ4 or kFmtQ8Q4.
+template <class T, int FMT>
+__global__ void __launch_bounds__(256)
+cache_write_kernel(const CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ out,
+                   int row_bytes) {
+    __shared__ uint64_t step[kRopeMaxDims / 2];
+    load_steps(tab, p.rotate, step);
+    const int chunks = p.dims / 8;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const bool in = id < (long long)p.n * chunks;
+    const int i = in ? (int)(id / chunks) : 0, c = in ? (int)(id % chunks) : 0;
+    float v[8];
+    load_chunk<T>(p, tab, step, i, c, v);
+    uint8_t* row = out + (long long)(p.row0 + i) * row_bytes;
+    if constexpr (FMT == kFmtF16) {
+        if (!in) return;
+        uint4 w;
+        w.x = pack_half2(v[0], v[1]);
+        w.y = pack_half2(v[2], v[3]);
+        w.z = pack_half2(v[4], v[5]);
+        w.w = pack_half2(v[6], v[7]);
+        *reinterpret_cast<uint4*>(row + 16 * c) = w;
+    } else {
+        // (dims is a multiple of 32: a block's four lanes lie in one warp and one row)
+        float m = 0.f, am = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (fabsf(v[k]) > am) {
+                am = fabsf(v[k]);
+                m = v[k];
+            }
+#pragma unroll
+        for (int off = 1; off <= 2; off <<= 1) {      // strictly larger, or equal from a lower lane
+            const float om = __shfl_xor_sync(0xffffffffu, m, off), oam = fabsf(om);
+            if (oam > am || (oam == am && (threadIdx.x & off))) {
+                am = oam;
+                m = om;
+            }
+        }
+        const int b = c / 4, l = c % 4;
+        auto scale_bytes = [&](uint8_t* part, int fmt, int dims, __half d16) {
+            const int cb = quant_code_bytes(fmt, dims), nb = dims / kQBlock;
+            if (l == 0) *reinterpret_cast<__half*>(part + cb + 2 * b) = d16;
+            if (b == 0 && l == 1)
+                for (int k = cb + 2 * nb; k < quant_row_bytes(fmt, dims); k += 2)
+                    *reinterpret_cast<uint16_t*>(part + k) = 0;
+        };
+        if constexpr (FMT == kFmtQ8 || FMT == kFmtQ8Q4) {
+            const __half d16 = __float2half_rn(am / 127.f);
+            const uint2 w = q8_codes(v, __half2float(d16));
+            if (in) {
+                *reinterpret_cast<uint2*>(row + 8 * c) = w;
+                scale_bytes(row, kFmtQ8, p.dims, d16);
+            }
+        }
+        if constexpr (FMT == kFmtQ4 || FMT == kFmtQ8Q4) {
+            __half d16 = __float2half_rn(m / -8.f);
+            if (__half2float(d16) == 0.f) d16 = __float2half_rn(0.f);
+            const uint2 w = q4_codes(v, __half2float(d16));
+            uint2 hi;                                   // values 16.. of the block: lanes 2, 3
+            hi.x = __shfl_xor_sync(0xffffffffu, w.x, 2);
+            hi.y = __shfl_xor_sync(0xffffffffu, w.y, 2);
+            uint8_t* part = row + (FMT == kFmtQ8Q4 ? quant_row_bytes(kFmtQ8, p.dims) : 0);
+            const int dims = FMT == kFmtQ8Q4 ? kValueDims : p.dims;
+            if (in && 8 * c < dims) {
+                if (l < 2) *reinterpret_cast<uint2*>(part + 16 * b + 8 * l) = make_uint2(w.x | hi.x << 4, w.y | hi.y << 4);
+                scale_bytes(part, kFmtQ4, dims, d16);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- e4m3 with a scale per block
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+// fp16 values of two e4m3 codes (exact).
+__device__ __forceinline__ __half2 e4m3x2_half2(uint32_t two) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return *reinterpret_cast<const __half2*>(&r);
+}
+
+constexpr int kE4M3Threads = 512;               // 64 rows x 8 lanes
+constexpr int kE4M3Held = 9;                    // steps of 64 dims held in registers: up to 576 dims
+
+// One CTA per block of 64 rows that the write touches; eight lanes a row, each taking every
+// eighth chunk of eight values. Up to 576 dims the loaded values stay in registers between
+// the block's maximum and the rounding; wider rows are loaded twice.
+template <class T, bool HELD>
+__global__ void __launch_bounds__(kE4M3Threads)
+cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ cache) {
+    __shared__ uint64_t step[kRopeMaxDims / 2];
+    __shared__ float warp_top[kE4M3Threads / 32];
+    load_steps(tab, p.rotate, step);
+    const int tid = threadIdx.x, r = tid / 8, l = tid % 8;
+    const int blk = p.row0 / kScaleBlock + blockIdx.x;
+    const int i = blk * kScaleBlock + r - p.row0;        // this lane's row of the written ones
+    const bool in = i >= 0 && i < p.n;
+    const int chunks = p.dims / 8;
+    uint8_t* base = cache + (long long)blk * (kScaleBlock + 1) * p.dims;
+    float* record = reinterpret_cast<float*>(base + kScaleBlock * p.dims);
+    const int old = blockIdx.x == 0 ? p.row0 % kScaleBlock : 0;   // rows kept from before
+    const float old_scale = old ? *record : 0.f;
+
+    float v[HELD ? kE4M3Held : 1][8];
+    float top = 0.f;
+    auto take = [&](const float (&u)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float a = fabsf(u[k]);
+            if (a <= 3.402823466e38f) top = fmaxf(top, a);        // finite
+        }
+    };
+    if (in) {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int s = 0; s < kE4M3Held; ++s)
+                if (8 * s + l < chunks) {
+                    load_chunk<T>(p, tab, step, i, 8 * s + l, v[s]);
+                    take(v[s]);
+                }
+        } else {
+            for (int c = l; c < chunks; c += 8) {
+                load_chunk<T>(p, tab, step, i, c, v[0]);
+                take(v[0]);
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (tid % 32 == 0) warp_top[tid / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kE4M3Threads / 32; ++w) top = fmaxf(top, warp_top[w]);
+    int e = scale_exponent(top);
+    if (old) {
+        const int was = (int)(__float_as_uint(old_scale) >> 23) - 127;
+        if (was >= e) {
+            e = min(was, kScaleExpMax);                   // (a record this library wrote)
+        } else if (r < old) {
+            // the earlier rows' codes, rounded again to the larger scale
+            const float down = pow2f(max(was, -kScaleExpMax) - e);
+            for (int c = l; c < chunks; c += 8) {
+                uint32_t* at = reinterpret_cast<uint32_t*>(base + (long long)r * p.dims + 8 * c);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const float2 a = __half22float2(e4m3x2_half2(at[w] & 0xffffu));
+                    const float2 b = __half22float2(e4m3x2_half2(at[w] >> 16));
+                    at[w] = e4m3x4(a.x * down, a.y * down, b.x * down, b.y * down);
+                }
+            }
+        }
+    }
+    const float inv = pow2f(-e);
+    if (tid < p.dims / 4) reinterpret_cast<uint32_t*>(record)[tid] = tid == 0 ? __float_as_uint(pow2f(e)) : 0u;
+    for (int k = tid + kE4M3Threads; k < p.dims / 4; k += kE4M3Threads) reinterpret_cast<uint32_t*>(record)[k] = 0u;
+    if (!in) return;
+    auto put = [&](int c, const float (&u)[8]) {
+        const uint2 w = make_uint2(e4m3x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv),
+                                   e4m3x4(u[4] * inv, u[5] * inv, u[6] * inv, u[7] * inv));
+        *reinterpret_cast<uint2*>(base + (long long)r * p.dims + 8 * c) = w;
+    };
+    if constexpr (HELD) {
+#pragma unroll
+        for (int s = 0; s < kE4M3Held; ++s)
+            if (8 * s + l < chunks) put(8 * s + l, v[s]);
+    } else {
+        for (int c = l; c < chunks; c += 8) {
+            load_chunk<T>(p, tab, step, i, c, v[0]);
+            put(c, v[0]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- reading back
+
+struct CacheRead {
+    const uint8_t* cache;
+    const int32_t* rows;                        // NULL: row0 + i
+    int row0, n, cache_rows;
+    int dims, out_dims;                         // stored values of the part, values read
+    int row_bytes, part_off;                    // formats 0-3: a stored row, where the part starts
+    long long out_ld;                           // in values
+    int fast;                                   // out's rows are 16-byte aligned
+};
+
+// Eight values per thread: chunk c of row i, value = code * scale in fp32, rounded once to
+// T. An index outside the cache reads as a row of zeros.
+template <class T, int FMT>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRead p, T* __restrict__ out) {
+    const int chunks = p.out_dims / 8;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (long long)p.n * chunks) return;
+    const int i = (int)(id / chunks), c = (int)(id % chunks);
+    const int row = p.rows ? __ldg(p.rows + i) : p.row0 + i;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    if (row >= 0 && row < p.cache_rows) {
+        if constexpr (FMT == kFmtF16) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.cache + (long long)row * p.row_bytes + 16 * c));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+                v[2 * k] = f.x;
+                v[2 * k + 1] = f.y;
+            }
+        } else if constexpr (FMT == kFmtE4M3) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.cache + e4m3_place(row) * p.dims + 8 * c));
+            const long long rec = (long long)(row / kScaleBlock) * (kScaleBlock + 1) + kScaleBlock;
+            const float s = __ldg(reinterpret_cast<const float*>(p.cache + rec * p.dims));
+            const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(e4m3x2_half2(u[k / 2] >> (16 * (k % 2)) & 0xffffu));
+                v[2 * k] = f.x * s;
+                v[2 * k + 1] = f.y * s;
+            }
+        } else {
+            const uint8_t* part = p.cache + (long long)row * p.row_bytes + p.part_off;
+            const float d = __half2float(*reinterpret_cast<const __half*>(
+                part + quant_code_bytes(FMT, p.dims) + 2 * (c / 4)));
+            if constexpr (FMT == kFmtQ8) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(part + 8 * c));
+                const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = d * (float)(int8_t)(u[k / 4] >> (8 * (k % 4)) & 0xffu);
+            } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(part + 16 * (c / 4) + 8 * (c % 2)));
+                const uint32_t u[2] = {w.x, w.y};
+                const int shift = c % 4 < 2 ? 0 : 4;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = d * (float)((int)(u[k / 4] >> (8 * (k % 4) + shift) & 0xfu) - 8);
+            }
+        }
+    }
+    T* dst = out + i * p.out_ld + 8 * c;
+    union { uint4 q[sizeof(T) / 2]; T e[8]; } o;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o.e[k] = from_f32<T>(v[k]);
+    if (p.fast) {
+#pragma unroll
+        for (int w = 0; w < (int)sizeof(T) / 2; ++w) reinterpret_cast<uint4*>(dst)[w] = o.q[w];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = o.e[k];
+    }
+}
+
+}  // namespace ds4sp

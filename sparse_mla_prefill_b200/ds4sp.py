@@ -44,8 +44,16 @@ class ds4sp_io(ctypes.Structure):
                 ("topk", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
+class ds4sp_rope_config(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int), ("offset", ctypes.c_int), ("layout", ctypes.c_int),
+                ("scaling", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_int), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_i64 = ctypes.c_longlong
 
 _SIGS = {
     "ds4sp_create": (_i32, [ctypes.POINTER(ds4sp_config), ctypes.POINTER(_vp)]),
@@ -69,6 +77,12 @@ _SIGS = {
                                           _i32, _vp, _vp]),
     "ds4sp_kv_row_bytes": (_i32, [_i32, _i32]),
     "ds4sp_quantize_kv": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
+    "ds4sp_rope": (_i32, [ctypes.POINTER(ds4sp_rope_config), _vp, _i32, _i32, _i32, _i32, _i64, _i64,
+                          _vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp]),
+    "ds4sp_cache_bytes": (_sz, [_i32, _i32, _i64]),
+    "ds4sp_cache_write": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i64,
+                                 ctypes.POINTER(ds4sp_rope_config), _vp, _i64, _i64, _vp]),
+    "ds4sp_cache_read": (_i32, [_vp, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _vp]),
     "ds4sp_probe_gather": (_i32, [_vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp]),
     "ds4sp_status_string": (ctypes.c_char_p, [_i32]),
     "ds4sp_last_error": (ctypes.c_char_p, []),
@@ -310,6 +324,111 @@ def ds4sp_quantize_kv(x, kv_format: int, out=None, stream=None):
     _check(load_library().ds4sp_quantize_kv(_ptr(x, "x", torch.float16), rows, dims, kv_format,
                                             _ptr(out, "out", torch.uint8), _stream(stream)),
            "ds4sp_quantize_kv")
+    return out
+
+
+# ------------------------------------------------------------------ rotary, cache rows
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+SCALE_BLOCK = 64      # rows of a kv_format 5 cache that share a scale
+
+
+def make_rope(dims: int, offset: int = 0, layout: int = 0, base: float = 10000.0, scaling: int = 0,
+              factor: float = 1.0, orig_len: int = 0, beta_fast: float = 0.0, beta_slow: float = 0.0,
+              mscale: float = 0.0) -> ds4sp_rope_config:
+    """A ds4sp_rope_config. layout: 0 = interleaved pairs, 1 = halves; scaling: 0 = none,
+    1 = linear, 2 = NTK, 3 = YaRN (include/ds4sp.h has the formulas)."""
+    return ds4sp_rope_config(dims, offset, layout, scaling, base, factor, orig_len, beta_fast, beta_slow,
+                             mscale)
+
+
+def _rows(t: torch.Tensor, name: str, dims: int) -> int:
+    """The dtype code of a strided device tensor of `dims` dimensions whose last one is
+    contiguous. It belongs to the current device, whose stream the call uses."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise Ds4spError(ERR_INVALID_ARG, name, "tensor must be on the current CUDA device")
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise Ds4spError(ERR_INVALID_ARG, name, f"expected {dims} dimensions, the last one contiguous")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise Ds4spError(ERR_INVALID_ARG, name, f"dtype {t.dtype}, expected float16, bfloat16 or float32")
+    return code
+
+
+def _int_rows(t: Optional[torch.Tensor], name: str, n: int) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != torch.cuda.current_device() or t.dtype != torch.int32 \
+            or not t.is_contiguous() or t.numel() != n:
+        raise Ds4spError(ERR_INVALID_ARG, name, f"expected a contiguous int32 tensor of {n} on the current device")
+    return t.data_ptr()
+
+
+def ds4sp_rope(x, rope: ds4sp_rope_config, out=None, positions=None, pos0: int = 0, pos_step: int = 1,
+               transpose: bool = False, stream=None):
+    """Turn the rotary part of x [n_tokens, heads, head_dim] (float16, bfloat16 or float32;
+    any token and head strides) and return ``out`` (of x's shape and type, allocated if None;
+    x itself for in place). positions: int32 [n_tokens], or None for pos0 + i * pos_step.
+    transpose: the transposed rotation, the gradient with respect to x."""
+    code = _rows(x, "x", 3)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif _rows(out, "out", 3) != code or out.shape != x.shape:
+        raise Ds4spError(ERR_INVALID_ARG, "out", f"expected {x.dtype} {tuple(x.shape)}")
+    n, heads, head = x.shape
+    xs, os_ = x.stride(), out.stride()
+    _check(load_library().ds4sp_rope(rope, x.data_ptr(), code, n, heads, head, xs[0], xs[1], out.data_ptr(),
+                                     os_[0], os_[1], _int_rows(positions, "positions", n), pos0, pos_step,
+                                     int(transpose), _stream(stream)), "ds4sp_rope")
+    return out
+
+
+def ds4sp_cache_bytes(kv_format: int, dims: int, rows: int) -> int:
+    return int(load_library().ds4sp_cache_bytes(kv_format, dims, rows))
+
+
+def _cache(cache: torch.Tensor, kv_format: int, dims: int) -> int:
+    """Rows that a cache tensor (uint8, or float16 rows) holds in a format."""
+    if not cache.is_cuda or cache.device.index != torch.cuda.current_device() or not cache.is_contiguous():
+        raise Ds4spError(ERR_INVALID_ARG, "cache", "expected a contiguous tensor on the current CUDA device")
+    if cache.dtype != torch.uint8 and not (kv_format == 0 and cache.dtype == torch.float16):
+        raise Ds4spError(ERR_INVALID_ARG, "cache", f"dtype {cache.dtype}, expected uint8 (or float16 rows)")
+    unit = SCALE_BLOCK if kv_format == 5 else 1
+    size = ds4sp_cache_bytes(kv_format, dims, unit)
+    if size == 0:
+        raise Ds4spError(ERR_INVALID_ARG, "cache", f"kv_format {kv_format} with rows of {dims} values")
+    return cache.numel() * cache.element_size() // size * unit
+
+
+def ds4sp_cache_write(cache, kv_format: int, x, row0: int, rope: Optional[ds4sp_rope_config] = None,
+                      positions=None, pos0: int = 0, pos_step: int = 1, stream=None) -> None:
+    """Store rows x [n, dims] (float16, bfloat16 or float32, any row stride) as rows row0 ..
+    of ``cache`` (uint8, ds4sp_cache_bytes(kv_format, dims, rows) bytes; float16 rows for
+    kv_format 0), after turning part of each (rope)."""
+    code = _rows(x, "x", 2)
+    n, dims = x.shape
+    rows = _cache(cache, kv_format, dims)
+    _check(load_library().ds4sp_cache_write(cache.data_ptr(), kv_format, dims, rows, row0, n, x.data_ptr(), code,
+                                            x.stride(0), rope, _int_rows(positions, "positions", n), pos0,
+                                            pos_step, _stream(stream)), "ds4sp_cache_write")
+
+
+def ds4sp_cache_read(cache, kv_format: int, dims: int, rows=None, row0: int = 0, n: Optional[int] = None,
+                     part: int = 0, out=None, dtype=torch.float16, stream=None):
+    """Rows ``rows`` (int32) or row0 .. row0+n-1 of ``cache`` as values: returns ``out``
+    ([n, dims], or [n, 512] for part 1, the value; allocated as ``dtype`` if None)."""
+    held = _cache(cache, kv_format, dims)
+    if n is None:
+        n = held - row0 if rows is None else rows.numel()
+    width = 512 if part == 1 else dims
+    if out is None:
+        out = torch.empty((max(n, 0), width), dtype=dtype, device=cache.device)
+    code = _rows(out, "out", 2)
+    if out.shape != (n, width):
+        raise Ds4spError(ERR_INVALID_ARG, "out", f"expected [{n}, {width}]")
+    _check(load_library().ds4sp_cache_read(cache.data_ptr(), kv_format, dims, held, _int_rows(rows, "rows", n),
+                                           row0, n, part, out.data_ptr(), code, out.stride(0), _stream(stream)),
+           "ds4sp_cache_read")
     return out
 
 
