@@ -109,7 +109,14 @@ typedef struct {
                             once to fp16) and otherwise computes as for fp16 rows; the
                             indexer keys (k_idx) stay fp16. Quantized formats need
                             exp_mode 0 and pv_mode 0, and top_k <= 1012 (format 2) or
-                            824 (format 3) (else DS4SP_ERR_UNSUPPORTED); other values are DS4SP_ERR_INVALID_ARG
+                            824 (format 3) (else DS4SP_ERR_UNSUPPORTED). 5 = 8-bit rows
+                            with a scale for each block of 64, as ds4sp_cache_write
+                            stores them (ds4sp_cache_bytes(5, 576, rows) bytes): the
+                            attention multiplies the e4m3 codes as they are, on the
+                            tcgen05 tensor cores, with the queries and the probabilities
+                            as sums of e4m3 terms (pv_mode 0: three terms of P, about 12
+                            bits; 1: five, about 20); it needs exp_mode 0 and attn_kernel
+                            0. Other values are DS4SP_ERR_INVALID_ARG
                             ("Q4_0 K/V cache" and "Q8 K / Q4 V", "perf(ds4): extend sparse
                             prefill scheduling to 10K", Production workflow and the
                             clean-head validation; the pages name the formats without

@@ -135,22 +135,22 @@ def stored_bytes(codes: np.ndarray, exp: np.ndarray) -> np.ndarray:
 
 # ------------------------------------------------------------------ attention
 
-def attention_rows(q_t: np.ndarray, rows: np.ndarray, scale: Optional[float] = None, d_v: int = 512) -> np.ndarray:
-    """One token's heads q_t [16, 576] over rows [n, 576]: softmax(scale q . row) @ row[:512]."""
+def attention_rows(q_t: np.ndarray, rows: np.ndarray, scale: Optional[float] = None, d_v: int = 512,
+                   absolute: bool = False) -> np.ndarray:
+    """One token's heads q_t [16, 576] over rows [n, 576]: softmax(scale q . row) @ row[:512]
+    (absolute: @ |row[:512]|, the size that rounding errors are measured against)."""
     rows = np.asarray(rows, dtype=np.float64)
     z = np.asarray(q_t, dtype=np.float64) @ rows.T * (1 / 24.0 if scale is None else scale)
     p = np.exp(z - z.max(1, keepdims=True))
-    return (p / p.sum(1, keepdims=True)) @ rows[:, :d_v]
+    v = np.abs(rows[:, :d_v]) if absolute else rows[:, :d_v]
+    return (p / p.sum(1, keepdims=True)) @ v
 
 
-def attention_tokens(q: np.ndarray, raw: np.ndarray, cmp: np.ndarray, topk: Optional[np.ndarray], t0: int,
-                     tokens, n_swa: int, scale: Optional[float] = None) -> np.ndarray:
-    """Tokens t0 + i (i in tokens) over their selected rows (topk[i], -1 dropped) and window."""
-    out = []
-    for i in tokens:
-        t = t0 + i
-        parts = [raw[max(0, t - n_swa + 1):t + 1]]
-        if topk is not None and topk.shape[1]:
-            parts.insert(0, cmp[topk[i][topk[i] >= 0]])
-        out.append(attention_rows(q[i], np.concatenate(parts), scale))
-    return np.stack(out)
+def attended(raw: np.ndarray, cmp: np.ndarray, topk: Optional[np.ndarray], t0: int, i: int, n_swa: int) -> np.ndarray:
+    """What token t0 + i attends of per-row arrays: its selected compressed rows (topk[i], -1
+    dropped), then its window of raw rows."""
+    t = t0 + i
+    parts = [raw[max(0, t - n_swa + 1):t + 1]]
+    if topk is not None and topk.shape[1]:
+        parts.insert(0, cmp[topk[i][topk[i] >= 0]])
+    return np.concatenate(parts)

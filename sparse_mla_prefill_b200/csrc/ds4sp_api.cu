@@ -25,6 +25,7 @@
 #include "probe_gather.cuh"
 #include "rope.cuh"
 #include "sparse_attn_mma.cuh"
+#include "sparse_attn_scaled.cuh"
 #include "sparse_attn_tc.cuh"
 #include "topk_radix.cuh"
 
@@ -175,8 +176,11 @@ int attn_max_topk(int kvf) {
 
 // Bytes of one row of kv_raw / kv_cmp in the handle's cache format.
 int kv_row_bytes_of(const ds4sp_config& c) {
-    return c.kv_format == 0 ? c.d_qk * 2 : quant_row_bytes(c.kv_format, c.d_qk);
+    return c.kv_format == 0 ? c.d_qk * 2 : c.kv_format == kFmtE4M3 ? c.d_qk : quant_row_bytes(c.kv_format, c.d_qk);
 }
+
+// Bytes from a cache's start that hold its first `rows` rows (kv_format 5: whole blocks).
+size_t kv_span(const ds4sp_config& c, int rows) { return ds4sp_cache_bytes(c.kv_format, c.d_qk, rows); }
 
 float scale_of(const ds4sp_config& c) {
     return c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt((float)c.d_qk);
@@ -670,6 +674,12 @@ ds4sp_status launch_attn(ds4sp_handle* h, const void* q, const void* kv_raw, con
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    tcattn::smem_bytes(attn::MAX_TOPK));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attention, tcgen05)");
+        for (const void* fn : {reinterpret_cast<const void*>(sparse_attn_scaled_kernel<3>),
+                               reinterpret_cast<const void*>(sparse_attn_scaled_kernel<5>)}) {
+            const cudaError_t es = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        scaled::SMEM_BYTES);
+            if (es != cudaSuccess) return cuda_fail(es, "cudaFuncSetAttribute(attention, scaled)");
+        }
         h->smem_set[kAttn] = true;
     }
     AttnParams p;
@@ -734,6 +744,12 @@ ds4sp_status launch_attn(ds4sp_handle* h, const void* q, const void* kv_raw, con
         const bool pdl = h->cfg.dependent_launch != 0;
         if (tc) {
             launch_k(pdl, sparse_attn_tc_kernel, g, dim3(tcattn::THREADS), smem, stream, p);
+        } else if (h->cfg.kv_format == kFmtE4M3) {
+            const dim3 bsc(scaled::THREADS);
+            if (h->cfg.pv_mode == 1)
+                launch_k(pdl, sparse_attn_scaled_kernel<5>, g, bsc, scaled::SMEM_BYTES, stream, p);
+            else
+                launch_k(pdl, sparse_attn_scaled_kernel<3>, g, bsc, scaled::SMEM_BYTES, stream, p);
         } else if (h->cfg.kv_format == kFmtQ8) {
             launch_k(pdl, sparse_attn_mma_kernel<false, false, kFmtQ8>, g, bs, smem, stream, p);
         } else if (h->cfg.kv_format == kFmtQ4) {
@@ -1038,14 +1054,14 @@ ds4sp_status ds4sp_create(const ds4sp_config* cfg, ds4sp_handle** out) {
         return fail(DS4SP_ERR_UNSUPPORTED, "attn_kernel 1 runs fp16 rows with exp_mode 0 and pv_mode 0");
     if (c.dependent_launch != 0 && c.dependent_launch != 1)
         return fail(DS4SP_ERR_INVALID_ARG, "dependent_launch %d (0 or 1)", c.dependent_launch);
-    if (c.kv_format < 0 || c.kv_format > 3)
-        return fail(DS4SP_ERR_INVALID_ARG, "kv_format %d (0 = fp16, 1 = Q8_0, 2 = Q4_0, 3 = Q8 K / Q4 V)",
-                    c.kv_format);
+    if ((c.kv_format < 0 || c.kv_format > 3) && c.kv_format != kFmtE4M3)
+        return fail(DS4SP_ERR_INVALID_ARG, "kv_format %d (0 = fp16, 1 = Q8_0, 2 = Q4_0, 3 = Q8 K / Q4 V, "
+                    "5 = e4m3 with a scale per block)", c.kv_format);
     if (c.kv_format >= 1 && c.kv_format <= 3 && c.top_k > attn_max_topk(c.kv_format))
         return fail(DS4SP_ERR_UNSUPPORTED, "kv_format %d supports top_k up to %d", c.kv_format,
                     attn_max_topk(c.kv_format));
-    if (c.kv_format != 0 && (c.exp_mode != 0 || c.pv_mode != 0))
-        return fail(DS4SP_ERR_UNSUPPORTED, "a quantized cache runs with exp_mode 0 and pv_mode 0");
+    if (c.kv_format != 0 && (c.exp_mode != 0 || (c.pv_mode != 0 && c.kv_format != kFmtE4M3)))
+        return fail(DS4SP_ERR_UNSUPPORTED, "a quantized cache runs with exp_mode 0, and kv_format 1 .. 3 with pv_mode 0");
     ds4sp_handle* h = new (std::nothrow) ds4sp_handle();
     if (!h) return fail(DS4SP_ERR_INVALID_ARG, "out of host memory");
     h->cfg = c;
@@ -1257,7 +1273,7 @@ ds4sp_status ds4sp_prefill_host(ds4sp_handle* h, int n_tokens, const ds4sp_io* h
     if (e != cudaSuccess) return cuda_fail(e, "ds4sp_prefill_host: ordering");
 
     const size_t q_row = (size_t)c.n_heads * c.d_qk * 2, qi_row = (size_t)c.n_idx_heads * c.d_idx * 2;
-    const size_t w_row = (size_t)c.n_idx_heads * 4, kv_row = (size_t)kv_row_bytes_of(c);
+    const size_t w_row = (size_t)c.n_idx_heads * 4;
     const size_t ki_row = (size_t)c.d_idx * 2, o_row = (size_t)c.n_heads * c.d_v * 4;
     const size_t tk_row = (size_t)c.top_k * 4;
     auto h2d = [&](const void* dst, const void* src, size_t off, size_t bytes) {
@@ -1272,17 +1288,21 @@ ds4sp_status ds4sp_prefill_host(ds4sp_handle* h, int n_tokens, const ds4sp_io* h
                                bytes, cudaMemcpyDeviceToHost, h->copy_out);
     };
     // Inputs: per step, its token rows and the KV rows it is the first to need.
-    int raw_done = 0, cmp_done = 0;
+    // (in kv_format 5 a row brings its whole block, with its scale).
+    int cmp_done = 0;
+    size_t raw_bytes = 0, cmp_bytes = 0;
     for (int i = 0; i < n_steps && e == cudaSuccess; ++i) {
         const int t0 = steps[i].t0, n = steps[i].n, t1 = t0 + n;
         e = h2d(dev->q, host->q, t0 * q_row, n * q_row);
         if (e == cudaSuccess && sel) e = h2d(dev->q_idx, host->q_idx, t0 * qi_row, n * qi_row);
         if (e == cudaSuccess && sel) e = h2d(dev->w, host->w, t0 * w_row, n * w_row);
-        if (e == cudaSuccess) e = h2d(dev->kv_raw, host->kv_raw, raw_done * kv_row, (t1 - raw_done) * kv_row);
-        raw_done = t1;
+        const size_t raw_need = kv_span(c, t1);
+        if (e == cudaSuccess) e = h2d(dev->kv_raw, host->kv_raw, raw_bytes, raw_need - raw_bytes);
+        raw_bytes = raw_need;
         const int cmp_need = sel ? nvis(t1 - 1, c.ratio) : 0;
         if (e == cudaSuccess && cmp_need > cmp_done) {
-            e = h2d(dev->kv_cmp, host->kv_cmp, cmp_done * kv_row, (cmp_need - cmp_done) * kv_row);
+            e = h2d(dev->kv_cmp, host->kv_cmp, cmp_bytes, kv_span(c, cmp_need) - cmp_bytes);
+            cmp_bytes = kv_span(c, cmp_need);
             if (e == cudaSuccess)
                 e = h2d(dev->k_idx, host->k_idx, cmp_done * ki_row, (cmp_need - cmp_done) * ki_row);
             cmp_done = cmp_need;
