@@ -127,6 +127,33 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
     }
 }
 
+// mbar_wait for a kernel of many waits that usually miss at first, by a little. The clock and
+// the abort word (a load from global memory, longer than most such waits) are first looked at
+// after 64 tests; and what follows the first test is one function out of line: a kernel whose
+// 25 waits were unrolled had 200 KB of instructions, and its roles spent their time fetching
+// them.
+__device__ __noinline__ bool mbar_wait_out_of_line(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+    unsigned long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1;; ++n) {
+        if ((n & 63u) == 0 || w.limit_ns == 0) {
+            const unsigned long long now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (launch_gave_up(w) || now - t0 >= w.limit_ns) {
+                give_up(w);
+                return false;
+            }
+        }
+        if (mbar_try_wait(bar, parity)) return true;
+    }
+}
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, const WaitCtl& w, bool& abort) {
+    if (abort) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    abort = !mbar_wait_out_of_line(bar, parity, w);
+    return !abort;
+}
+
 // Wait for a phase that completes without any other role's help (bulk copies this
 // thread issued, MMAs it committed), before the memory they write is released. Bounded
 // by kDrainLimitNs only; records kStatusTimeout if even that runs out.

@@ -29,9 +29,9 @@
 // it lies, the MN-major A of O^T. Slabs form a ring of nine: O^T frees them one by one (its
 // tile m reads slab m only), and the gather of a later unit follows on its heels.
 //
-// Roles: warps 0-3 softmax (a row per thread), 4-7 the queries' terms and the output, 8-11
-// gather (16-byte cp.async), warp 12 issues the MMAs: S of unit g + 1 before O^T of unit g,
-// so that the softmax of a unit has a whole unit's tensor time to finish.
+// Roles: warps 0-7 softmax, 8-11 the queries' terms and the output, 12-15 gather (16-byte
+// cp.async), warp 16 issues S and warp 17 O^T: an MMA of this size is short
+// against a wait's latency, and with two issuers each one's waits run under the other's MMAs.
 // The reference ref_h is the first unit's maximum and is raised (O and the sums rescaled)
 // only when a unit exceeds it by 2^8: e4m3 holds weights up to 448.
 // Every wait is bounded; a wait that gives up sets the launch's abort word and every role
@@ -55,10 +55,11 @@ constexpr int ROPES = 3;                        // ring of the rows' last 64 dim
 constexpr int SLAB = M * 128, ROPE = M * 64;
 constexpr int QROWS = QT * H;
 constexpr int QSLAB = QROWS * 128, QBYTES = TILES * QSLAB + QROWS * 64;
-constexpr int SWARPS = 4, EWARPS = 4, PWARPS = 4;
-constexpr int EWARP0 = SWARPS, PWARP0 = EWARP0 + EWARPS, MWARP = PWARP0 + PWARPS;
-constexpr int THREADS = (MWARP + 1) * 32;
-constexpr int SOFTMAX_BAR = 1;
+constexpr int SWARPS = 8, EWARPS = 4, PWARPS = 4;
+constexpr int HG = H / 2;                       // heads of a softmax group of four warps
+constexpr int EWARP0 = SWARPS, PWARP0 = EWARP0 + EWARPS, SMMA = PWARP0 + PWARPS, OMMA = SMMA + 1;
+constexpr int THREADS = (OMMA + 1) * 32;
+constexpr int SOFTMAX_BAR = 1;                  // and 2: one per group
 constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference
 
 constexpr int OFF_SLAB = 0;
@@ -67,9 +68,9 @@ constexpr int OFF_Q = OFF_ROPE + ROPES * ROPE;
 constexpr int OFF_P = OFF_Q + QBYTES;                        // two buffers of NT x 128 rows x 16 bytes
 constexpr int OFF_SCALE = OFF_P + 2 * 5 * M * H;             // rows' scales, one array per rope slot
 constexpr int OFF_QS = OFF_SCALE + ROPES * M * 4;            // heads' logit factors, four tokens
-constexpr int OFF_RED = OFF_QS + 4 * H * 4;                  // per softmax warp: maxima
-constexpr int OFF_SUM = OFF_RED + SWARPS * H * 4;            // per softmax warp: sums, two tokens
-constexpr int OFF_REF = OFF_SUM + 2 * SWARPS * H * 4;        // references, two tokens
+constexpr int OFF_RED = OFF_QS + 4 * H * 4;                  // per warp of a group: maxima
+constexpr int OFF_SUM = OFF_RED + 4 * H * 4;                 // per warp of a group: sums, two tokens
+constexpr int OFF_REF = OFF_SUM + 2 * 4 * H * 4;             // references, two tokens
 constexpr int OFF_BAR = OFF_REF + 2 * H * 4;
 // barriers
 constexpr int B_SLAB_FULL = 0, B_SLAB_EMPTY = B_SLAB_FULL + SLOTS, B_ROPE_FULL = B_SLAB_EMPTY + SLOTS,
@@ -105,30 +106,54 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool tr) {
     return 1u << 4 | (tr ? 3u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
-    const uint32_t acc = accumulate ? 1u : 0u;
+// n (1 .. 4) MMAs in a row whose operands' addresses step by A_STEP and B_STEP bytes, executed
+// by a whole warp and issued by its elected lane (the same one every time). acc0: whether the
+// first accumulates; the others do.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc0, int n) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n\t.reg .pred p, e, q, t;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, %6;\n\tadd.s64 b, %2, %7;\n\tsetp.gt.and.s32 q, %5, 1, e;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\tsetp.gt.and.s32 q, %5, 2, e;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\tsetp.gt.and.s32 q, %5, 3, e;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(id), "r"(acc0), "r"(n), "n"(A_STEP >> 4), "n"(B_STEP >> 4)
+        : "memory");
+}
+// An arrival when all MMAs issued so far complete.
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
 // Shared-memory writes of this thread (or writes it has acquired) before later tcgen05 reads.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-        : "memory");
+// This thread's TMEM lane, eight consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Ties registers written by an earlier tcgen05.ld to a point after tmem_ld_wait().
+__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[8]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
 __device__ __forceinline__ void regs_after_wait(uint32_t (&r)[16]) {
     asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                       "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
@@ -140,18 +165,37 @@ __device__ __forceinline__ float warp_max(float v) {         // NaNs are ignored
     return r;
 }
 
-// This CTA's units in order: item idx, the u-th of its nu units of rows. In split mode an
-// item is one unit of 32 rows (token_rows).
+// A work item: a token's rows, or in split mode (few tokens) 32 of them. Row r of the item
+// is a selected compressed row for r < nsel, then window row s_lo + r - nsel.
+struct Item {
+    int i, t, nv;              // token of the call, absolute token, compressed rows it sees
+    int nsel, s_lo;
+    int row0, rows;            // the item's rows among the token's, [row0, row0 + rows)
+};
+
+// Out of line: every role walks the items, and takes one per token.
+__device__ __noinline__ Item take_item(const AttnParams& p, int idx) {
+    const TokenRows tr = token_rows(p, idx);
+    Item it;
+    it.i = tr.i;
+    it.t = tr.t;
+    it.nv = tr.nv;
+    it.nsel = tr.nsel;
+    it.s_lo = tr.s_lo;
+    it.row0 = p.split ? SPLIT_ROWS * tr.u0 : 0;
+    it.rows = p.split ? min(SPLIT_ROWS, tr.nrows - it.row0) : tr.nrows;
+    return it;
+}
+
+// This CTA's units in order: rows [128 u, 128 u + rows()) of its m-th item.
 struct Cursor {
-    int m, idx, u, nu;
-    TokenRows tr;
+    int m, idx, u;
+    Item it;
     bool valid;
     __device__ __forceinline__ void take(const AttnParams& p) {
         valid = idx < p.n_items;
         u = 0;
-        if (!valid) return;
-        tr = token_rows(p, idx);
-        nu = p.split ? 1 : (tr.nrows + M - 1) / M;
+        if (valid) it = take_item(p, idx);
     }
     __device__ __forceinline__ void start(const AttnParams& p) {
         m = 0;
@@ -163,14 +207,22 @@ struct Cursor {
         idx += gridDim.x;
         take(p);
     }
+    __device__ __forceinline__ bool last() const { return M * (u + 1) >= it.rows; }
     __device__ __forceinline__ void advance(const AttnParams& p) {
-        if (++u == nu) next_item(p);
+        if (last()) next_item(p);
+        else ++u;
     }
-    __device__ __forceinline__ int first_row(const AttnParams& p) const { return p.split ? SPLIT_ROWS * tr.u0 : M * u; }
-    __device__ __forceinline__ int rows(const AttnParams& p) const {      // of this unit
-        return min(p.split ? SPLIT_ROWS : M, tr.nrows - first_row(p));
-    }
+    __device__ __forceinline__ int rows() const { return min(M, it.rows - M * u); }
 };
+
+// fp16 -> e4m3 codes of a pair, and what they leave, times 16 (exact: the difference of an
+// fp16 value and its rounding to fewer bits is an fp16 value).
+__device__ __forceinline__ uint32_t e4m3x2_of(__half2 v) {
+    return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&v), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 left16(__half2 v, uint32_t codes) {
+    return __hmul2(__hsub2(v, e4m3x2_half2(codes)), __float2half2_rn(16.f));
+}
 
 }  // namespace scaled
 
@@ -193,7 +245,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         }
         for (int s = 0; s < ROPES; ++s) {
             mbar_init(bar(B_ROPE_FULL + s), PWARPS * 32);
-            mbar_init(bar(B_ROPE_EMPTY + s), 1 + SWARPS);    // S, and the scales' readers
+            mbar_init(bar(B_ROPE_EMPTY + s), SWARPS);        // the softmax: S has run, the scales are read
         }
         mbar_init(bar(B_Q_FULL), EWARPS);
         mbar_init(bar(B_Q_EMPTY), 1);
@@ -207,10 +259,10 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             mbar_init(bar(B_L_FULL + i), SWARPS);
             mbar_init(bar(B_L_EMPTY + i), EWARPS);
         }
-        mbar_init(bar(B_DONE), 1);
+        mbar_init(bar(B_DONE), 2);
         fence_mbar_init();
     }
-    if (warp == MWARP) {
+    if (warp == SMMA) {
         tmem_alloc(smem_u32(tmem_ptr), 512);
         tmem_relinquish();
     }
@@ -222,43 +274,57 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
     grid_dependents_launch();
 
     bool abort = false;
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, p.wc, abort); };
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait_soon(bar(b), parity, p.wc, abort); };
     Cursor c;
     c.start(p);
 
-    if (warp >= PWARP0 && warp < MWARP) {
+    if (warp >= PWARP0 && warp < SMMA) {
         // ================================================================ gather
         const int pw = warp - PWARP0, r = 32 * pw + lane;    // this thread resolves row r
-        // Place of the unit's row r: 2 * place + 1 (compressed) or 2 * place; -1: none. The
-        // top-k entry of a unit is fetched a unit ahead.
-        auto entry = [&](const Cursor& cu) {
-            const int gr = cu.first_row(p) + r;
-            return cu.valid && gr < cu.tr.nsel && r < cu.rows(p) ? __ldg(p.topk + (size_t)cu.tr.i * p.k + gr) : -1;
-        };
-        auto resolve = [&](const Cursor& cu, int j) {
-            const int gr = cu.first_row(p) + r;
-            if (r >= cu.rows(p)) return -1;
-            if (gr >= cu.tr.nsel) {
-                const int row = cu.tr.s_lo + gr - cu.tr.nsel;
-                return 2 * (int)e4m3_place(row);
-            }
-            const bool in = j >= 0 && j < (p.vis_mask ? p.mask_cols : cu.tr.nv);
-            if (!in && !(p.vis_mask && j == -1)) record_status(p.wc.status, kStatusBounds);
-            if (!in || (p.vis_mask && p.vis_mask[(size_t)cu.tr.t * p.mask_ld + j] == 0)) return -1;
-            return 2 * (int)e4m3_place(j) + 1;
-        };
         const uint8_t* raw = reinterpret_cast<const uint8_t*>(p.kv_raw);
         const uint8_t* cmp = reinterpret_cast<const uint8_t*>(p.kv_cmp);
+        // The top-k entry of a unit's row r, fetched a unit ahead.
+        auto entry = [&](const Cursor& cu) {
+            const int gr = cu.it.row0 + M * cu.u + r;
+            return cu.valid && r < cu.rows() && gr < cu.it.nsel ? __ldg(p.topk + (size_t)cu.it.i * p.k + gr) : -1;
+        };
+        // Where row r's values are, and its scale. A row that is not attended (behind the
+        // last, or skipped) gets scale 0, so weight 0, and the token's own raw row as its
+        // values: that row is attended too, so 0 times its values adds nothing, whatever
+        // they are.
+        auto resolve = [&](const Cursor& cu, int j, bool& ok) {
+            const int gr = cu.it.row0 + M * cu.u + r;
+            ok = r < cu.rows();
+            int row = cu.it.t;
+            if (ok && gr >= cu.it.nsel) row = cu.it.s_lo + gr - cu.it.nsel;
+            if (!ok || gr >= cu.it.nsel) return raw + (size_t)e4m3_place(row) * DQK;
+            ok = j >= 0 && j < (p.vis_mask ? p.mask_cols : cu.it.nv);
+            if (!ok && !(p.vis_mask && j == -1)) record_status(p.wc.status, kStatusBounds);
+            if (ok && p.vis_mask) ok = p.vis_mask[(size_t)cu.it.t * p.mask_ld + j] != 0;
+            return ok ? cmp + (size_t)e4m3_place(j) * DQK : raw + (size_t)e4m3_place(row) * DQK;
+        };
+        // A warp copies 32 rows, four at a time: lane l takes chunk l % 8 of row l / 8 of the
+        // four, so an instruction covers four whole 128-byte lines.
+        const int ch = lane & 7, r4 = lane >> 3;
+        const uint32_t to_slab[2] = {(uint32_t)(32 * pw * 128 + r4 * 128 + ((ch ^ r4) << 4)),
+                                     (uint32_t)(32 * pw * 128 + r4 * 128 + ((ch ^ (r4 + 4)) << 4))};
+        const uint32_t to_rope = 32 * pw * 64 + r4 * 64;
         int slot = 0, rope = 0;
         uint32_t slab_phase = 1, rope_phase = 1;
         int j = entry(c);
         while (c.valid) {
-            const int place = resolve(c, j);
-            const bool copied = 32 * pw < c.rows(p);         // O^T reads whole groups of 32 rows
-            Cursor nx = c;
-            nx.advance(p);
-            j = entry(nx);
-            c = nx;
+            bool ok;
+            const uint8_t* mine = resolve(c, j, ok);
+            const bool copied = 32 * pw < c.rows();          // O^T reads whole groups of 32 rows
+            const int place = c.it.row0 + M * c.u + r;
+            const int row = place < c.it.nsel ? j : c.it.s_lo + place - c.it.nsel;
+            const uint8_t* scale = (place < c.it.nsel ? cmp : raw) + ((size_t)(row / kScaleBlock) * (kScaleBlock + 1) + kScaleBlock) * DQK;
+            const uint8_t* src[8];
+#pragma unroll
+            for (int it = 0; it < 8; ++it)
+                src[it] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * it + r4)) + ch * 16;
+            c.advance(p);
+            j = entry(c);
 #pragma unroll 1
             for (int s = 0; s < TILES; ++s) {
                 if (!__all_sync(0xffffffffu, wait(B_SLAB_EMPTY + slot, slab_phase))) {
@@ -266,14 +332,9 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     break;
                 }
                 if (copied) {
-                    const uint32_t dst = base + OFF_SLAB + slot * SLAB + 32 * pw * 128;
+                    const uint32_t dst = base + OFF_SLAB + slot * SLAB;
 #pragma unroll
-                    for (int it = 0; it < 8; ++it) {         // four rows of 128 bytes
-                        const int rl = 4 * it + (lane >> 3), ch = lane & 7;
-                        const int pl = __shfl_sync(0xffffffffu, place, rl);
-                        const uint8_t* src = (pl & 1 ? cmp : raw) + (size_t)(max(pl, 0) >> 1) * DQK + s * 128 + ch * 16;
-                        cp_async_16(dst + rl * 128 + ((ch ^ (rl & 7)) << 4), pl < 0 ? raw : src, pl >= 0);
-                    }
+                    for (int it = 0; it < 8; ++it) cp_async_16(dst + to_slab[it & 1] + it * 512, src[it] + s * 128, true);
                 }
                 cp_async_arrive_noinc(bar(B_SLAB_FULL + slot));
                 if (++slot == SLOTS) {
@@ -282,25 +343,15 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 }
             }
             if (abort || !__all_sync(0xffffffffu, wait(B_ROPE_EMPTY + rope, rope_phase))) break;
-            if (copied) {
-                const uint32_t dst = base + OFF_ROPE + rope * ROPE + 32 * pw * 64;
+            if (copied && ch < 4) {
+                const uint32_t dst = base + OFF_ROPE + rope * ROPE + to_rope;
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {             // eight rows of 64 bytes
-                    const int rl = 8 * it + (lane >> 2), ch = lane & 3;
-                    const int pl = __shfl_sync(0xffffffffu, place, rl);
-                    const uint8_t* src = (pl & 1 ? cmp : raw) + (size_t)(max(pl, 0) >> 1) * DQK + DV + ch * 16;
-                    cp_async_16(dst + rl * 64 + ((ch ^ ((rl >> 1) & 3)) << 4), pl < 0 ? raw : src, pl >= 0);
-                }
+                for (int it = 0; it < 8; ++it)
+                    cp_async_16(dst + it * 256 + ((ch ^ ((2 * it + (r4 >> 1)) & 3)) << 4), src[it] + DV, true);
             }
-            {
-                // The row's scale, 0 for no row: place q of a block's row lies in block q / 65.
-                const int q = max(place, 0) >> 1;
-                const uint8_t* src = (place & 1 ? cmp : raw) + ((size_t)(q / (kScaleBlock + 1)) * (kScaleBlock + 1) + kScaleBlock) * DQK;
-                const int n = place >= 0 ? 4 : 0;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + OFF_SCALE + (rope * M + r) * 4),
-                             "l"(place >= 0 ? src : raw), "r"(n)
-                             : "memory");
-            }
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + OFF_SCALE + (rope * M + r) * 4),
+                         "l"(ok ? scale : raw), "r"(ok ? 4 : 0)
+                         : "memory");
             cp_async_arrive_noinc(bar(B_ROPE_FULL + rope));
             if (++rope == ROPES) {
                 rope = 0;
@@ -317,119 +368,103 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         }
         cp_async_commit();
         cp_async_wait<0>();
-    } else if (warp == MWARP) {
-        // ================================================================ MMA issuer
-        if (lane == 0) {
+    } else if (warp >= SMMA) {
+        // ================================================================ MMA issuers
+        auto wait_w = [&](int b, uint32_t parity) {          // the whole warp gives up together
+            abort = !__all_sync(0xffffffffu, wait(b, parity));
+            return !abort;
+        };
+        if (warp == SMMA) {                                  // S of each unit
             int slot = 0, rope = 0;
             uint32_t slab_phase = 0, rope_phase = 0;
-            int pv_slot = 0, pv_rows = 0;
-            bool pv_first = false, pv_last = false;
-            int pv_m = 0;
-            // O^T of unit g: its weights, the slabs from pv_slot on.
-            auto issue_o = [&](int g) {
-                if (!wait(B_P_FULL + (g & 1), (g >> 1) & 1)) return false;
-                if (pv_first && !wait(B_O_EMPTY, (pv_m & 1) ^ 1)) return false;
-                tc_fence_after();
-                const uint64_t b0 = desc_at(DESC_P, base + OFF_P + (g & 1) * PBUF);
-                const int steps = (pv_rows + 31) / 32;
-#pragma unroll 1
-                for (int t = 0; t < TILES; ++t) {
-                    const uint64_t a0 = desc_at(DESC_128, base + OFF_SLAB + pv_slot * SLAB);
-                    const uint32_t d = tmem + TM_O + t * OC;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < steps) umma_e4m3(d, a0 + k * (32 * 128 >> 4), b0 + k * (32 * H >> 4), idesc(OC, true), !pv_first || k > 0);
-                    umma_commit(bar(B_SLAB_EMPTY + pv_slot));
-                    if (++pv_slot == SLOTS) pv_slot = 0;
-                }
-                umma_commit(bar(B_P_EMPTY + (g & 1)));
-                if (pv_last) umma_commit(bar(B_O_FULL));
-                return true;
-            };
-            int g = 0;
-            for (; c.valid; ++g) {
-                if (c.u == 0 && !wait(B_Q_FULL, c.m & 1)) break;
-                if (!wait(B_S_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1)) break;
+            for (int g = 0; c.valid && !abort; ++g, c.advance(p)) {
+                if (c.u == 0 && !wait_w(B_Q_FULL, c.m & 1)) break;
+                if (!wait_w(B_S_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + TM_S + (g & 1) * QROWS;
-                bool ok = true;
 #pragma unroll 1
-                for (int s = 0; s < TILES && ok; ++s) {
-                    ok = wait(B_SLAB_FULL + slot, slab_phase);
-                    if (!ok) break;
+                for (int s = 0; s < TILES; ++s) {
+                    if (!wait_w(B_SLAB_FULL + slot, slab_phase)) break;
                     fence_async_proxy();
-                    const uint64_t a0 = desc_at(DESC_128, base + OFF_SLAB + slot * SLAB);
-                    const uint64_t b0 = desc_at(DESC_128, base + OFF_Q + s * QSLAB);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_e4m3(d, a0 + 2 * k, b0 + 2 * k, idesc(QROWS, false), s > 0 || k > 0);
+                    umma_e4m3<32, 32>(d, desc_at(DESC_128, base + OFF_SLAB + slot * SLAB),
+                                      desc_at(DESC_128, base + OFF_Q + s * QSLAB), idesc(QROWS, false), s, 4);
                     if (++slot == SLOTS) {
                         slot = 0;
                         slab_phase ^= 1;
                     }
                 }
-                if (!ok || !wait(B_ROPE_FULL + rope, rope_phase)) break;
+                if (abort || !wait_w(B_ROPE_FULL + rope, rope_phase)) break;
                 fence_async_proxy();
-                {
-                    const uint64_t a0 = desc_at(DESC_64, base + OFF_ROPE + rope * ROPE);
-                    const uint64_t b0 = desc_at(DESC_64, base + OFF_Q + TILES * QSLAB);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) umma_e4m3(d, a0 + 2 * k, b0 + 2 * k, idesc(QROWS, false), true);
-                }
-                umma_commit(bar(B_S_FULL + (g & 1)));
-                umma_commit(bar(B_ROPE_EMPTY + rope));
+                umma_e4m3<32, 32>(d, desc_at(DESC_64, base + OFF_ROPE + rope * ROPE),
+                                  desc_at(DESC_64, base + OFF_Q + TILES * QSLAB), idesc(QROWS, false), 1, 2);
+                commit_elected(bar(B_S_FULL + (g & 1)));
+                if (c.last()) commit_elected(bar(B_Q_EMPTY));
                 if (++rope == ROPES) {
                     rope = 0;
                     rope_phase ^= 1;
                 }
-                const bool last = c.u + 1 == c.nu;
-                if (last) umma_commit(bar(B_Q_EMPTY));
-                if (g > 0 && !issue_o(g - 1)) break;
-                pv_rows = c.rows(p);
-                pv_first = c.u == 0;
-                pv_last = last;
-                pv_m = c.m;
-                c.advance(p);
             }
-            if (!abort && g > 0) issue_o(g - 1);
-            umma_commit(bar(B_DONE));
-            mbar_wait_drain(bar(B_DONE), 0, p.wc);
+        } else {                                             // O^T
+            int slot = 0;
+            for (int g = 0; c.valid && !abort; ++g, c.advance(p)) {
+                const int b = g & 1, steps = (c.rows() + 31) / 32;
+                const bool first = c.u == 0;
+                if (!wait_w(B_P_FULL + b, (g >> 1) & 1)) break;
+                if (first && !wait_w(B_O_EMPTY, (c.m & 1) ^ 1)) break;
+                tc_fence_after();
+                const uint64_t b0 = desc_at(DESC_P, base + OFF_P + b * PBUF);
+                const uint32_t d = tmem + TM_O;
+#pragma unroll 1
+                for (int t = 0; t < TILES; ++t) {
+                    umma_e4m3<32 * 128, 32 * H>(d + t * OC, desc_at(DESC_128, base + OFF_SLAB + slot * SLAB), b0,
+                                                idesc(OC, true), !first, steps);
+                    commit_elected(bar(B_SLAB_EMPTY + slot));
+                    if (++slot == SLOTS) slot = 0;
+                }
+                commit_elected(bar(B_P_EMPTY + b));
+                if (c.last()) commit_elected(bar(B_O_FULL));
+            }
         }
+        commit_elected(bar(B_DONE));
+        if (lane == 0) mbar_wait_drain(bar(B_DONE), 0, p.wc);
         __syncwarp();
     } else if (warp < SWARPS) {
         // ================================================================ softmax
-        const int r = tid;                                   // this thread's row of each unit
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;  // the warp's TMEM lanes
+        // Two groups of four warps, eight heads each: a thread has one row of each unit.
+        const int hg = warp / 4, qd = warp % 4, r = 32 * qd + lane;
+        const uint32_t lanes = (uint32_t)(32 * qd) << 16;    // the warp's TMEM lanes
         const float* scales = reinterpret_cast<const float*>(smem + OFF_SCALE);
-        const float* qs = reinterpret_cast<const float*>(smem + OFF_QS);
-        float* red = reinterpret_cast<float*>(smem + OFF_RED);
-        float ref[H], sum[H], cq[H];
+        const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + hg * HG;
+        float* red = reinterpret_cast<float*>(smem + OFF_RED) + hg * HG;
+        const int group_bar = SOFTMAX_BAR + hg;
+        float ref[HG], sum[HG], cq[HG];
         int rope = 0;
         uint32_t rope_phase = 0;
         for (int g = 0; c.valid; ++g, c.advance(p)) {
             const bool first = c.u == 0;
             wait(B_ROPE_FULL + rope, rope_phase);
+            const float sv = scales[rope * M + r];
             wait(B_S_FULL + (g & 1), (g >> 1) & 1);
             __syncwarp();
             tc_fence_after();
-            float acc[H];
+            float acc[HG];
             {
-                uint32_t d0[16], d1[16], d2[16];
-                const uint32_t at = tmem + lanes + TM_S + (g & 1) * QROWS;
-                tmem_ld_x16(at, d0);
-                tmem_ld_x16(at + 16, d1);
-                tmem_ld_x16(at + 32, d2);
+                uint32_t d0[8], d1[8], d2[8];
+                const uint32_t at = tmem + lanes + TM_S + (g & 1) * QROWS + hg * HG;
+                tmem_ld_x8(at, d0);
+                tmem_ld_x8(at + H, d1);
+                tmem_ld_x8(at + 2 * H, d2);
                 tmem_ld_wait();
                 regs_after_wait(d0);
                 regs_after_wait(d1);
                 regs_after_wait(d2);
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                for (int h = 0; h < HG; ++h)
                     acc[h] = fmaf(fmaf(__uint_as_float(d2[h]), 0.0625f, __uint_as_float(d1[h])), 0.0625f, __uint_as_float(d0[h]));
             }
-            const float sv = scales[rope * M + r];
             if (first) {
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
+                for (int h = 0; h < HG; ++h) {
                     cq[h] = qs[(c.m & 3) * H + h];
                     ref[h] = 0.f;
                     sum[h] = 0.f;
@@ -450,22 +485,22 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             const float lsv = (float)sexp;                   // log2 of the row's scale
             float top = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
+            for (int h = 0; h < HG; ++h) {
                 acc[h] = fmaf(acc[h], cq[h] * sv, lsv);      // log2 of the row's weight
                 top = fmaxf(top, acc[h] - ref[h]);
             }
-            if (named_barrier_or(SOFTMAX_BAR, SWARPS * 32, first || abort || (valid && top > HEADROOM))) {
+            if (named_barrier_or(group_bar, 128, first || abort || (valid && top > HEADROOM))) {
                 // A new reference: the first unit's maximum, or one raised by this unit.
-                if (named_barrier_or(SOFTMAX_BAR, SWARPS * 32, abort)) break;
+                if (named_barrier_or(group_bar, 128, abort)) break;
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
+                for (int h = 0; h < HG; ++h) {
                     const float mx = warp_max(valid ? acc[h] : -INFINITY);
-                    if (lane == 0) red[warp * H + h] = mx;
+                    if (lane == 0) red[qd * H + h] = mx;
                 }
-                named_barrier(SOFTMAX_BAR, SWARPS * 32);
-                float alpha[H];
+                named_barrier(group_bar, 128);
+                float alpha[HG];
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
+                for (int h = 0; h < HG; ++h) {
                     const float mu = fmaxf(fmaxf(red[h], red[H + h]), fmaxf(red[2 * H + h], red[3 * H + h]));
                     const float was = first ? (mu > -INFINITY ? mu : 0.f) : ref[h];
                     ref[h] = mu > was + HEADROOM ? mu : was;
@@ -478,54 +513,56 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int col = 0; col < TILES * OC; col += H) {
-                        uint32_t o[16];
-                        tmem_ld_x16(tmem + lanes + TM_O + col, o);
+                    for (int col = hg * HG; col < TILES * OC; col += H) {
+                        uint32_t o[8];
+                        tmem_ld_x8(tmem + lanes + TM_O + col, o);
                         tmem_ld_wait();
                         regs_after_wait(o);
 #pragma unroll
-                        for (int h = 0; h < H; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
-                        tmem_st_x16(tmem + lanes + TM_O + col, o);
+                        for (int h = 0; h < HG; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
+                        tmem_st_x8(tmem + lanes + TM_O + col, o);
                     }
                     tmem_st_wait();
                 }
             }
             // Weights, their share of the sums, and their terms.
-            const float inv = __uint_as_float((uint32_t)(127 - sexp) << 23);   // 1 / s_r
+            const float inv = valid ? __uint_as_float((uint32_t)(127 - sexp) << 23) : 0.f;   // 1 / s_r
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
+            for (int h = 0; h < HG; ++h) {
                 const float w = valid ? fast_exp2(acc[h] - ref[h]) : 0.f;
                 acc[h] = w;
-                sum[h] = fmaf(w, valid ? inv : 0.f, sum[h]);
+                sum[h] = fmaf(w, inv, sum[h]);
+            }
+            // w = hi + lo, two fp16 values: three terms hold hi, and two more (NT = 5) what it
+            // leaves, times 16^3.
+            uint32_t codes[NT][2];
+#pragma unroll
+            for (int q = 0; q < HG / 2; ++q) {
+                uint32_t tc[NT];
+                __half2 v = __floats2half2_rn(acc[2 * q], acc[2 * q + 1]);
+                const float2 hi = __half22float2(v);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t == 3) v = __floats2half2_rn((acc[2 * q] - hi.x) * 4096.f, (acc[2 * q + 1] - hi.y) * 4096.f);
+                    tc[t] = e4m3x2_of(v);
+                    if (t != 2 && t + 1 < NT) v = left16(v, tc[t]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) codes[t][q / 2] = q & 1 ? __byte_perm(codes[t][q / 2], tc[t], 0x5410) : tc[t];
             }
             wait(B_P_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1);   // O^T of the unit before last
             __syncwarp();
-            const uint32_t prow = base + OFF_P + (g & 1) * PBUF + r * H;
+            uint8_t* prow = smem + OFF_P + (g & 1) * PBUF + r * H + hg * HG;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                uint32_t w4[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    w4[q] = e4m3x4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
-                    if (t + 1 < NT) {                        // what this term leaves, times 16
-                        const float2 lo = __half22float2(e4m3x2_half2(w4[q] & 0xffffu));
-                        const float2 hi = __half22float2(e4m3x2_half2(w4[q] >> 16));
-                        acc[4 * q] = (acc[4 * q] - lo.x) * 16.f;
-                        acc[4 * q + 1] = (acc[4 * q + 1] - lo.y) * 16.f;
-                        acc[4 * q + 2] = (acc[4 * q + 2] - hi.x) * 16.f;
-                        acc[4 * q + 3] = (acc[4 * q + 3] - hi.y) * 16.f;
-                    }
-                }
-                st_shared_v4(prow + t * (M * H), make_uint4(w4[0], w4[1], w4[2], w4[3]));
-            }
+            for (int t = 0; t < NT; ++t) *reinterpret_cast<uint2*>(prow + t * (M * H)) = make_uint2(codes[t][0], codes[t][1]);
             fence_async_proxy();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_P_FULL + (g & 1)));
-            if (c.u + 1 == c.nu) {
-                // The item's sums: 16 heads over 32 lanes, halving the heads a lane holds.
+            if (c.last()) {
+                // The item's sums: eight heads over 32 lanes, halving the heads a lane holds.
 #pragma unroll
-                for (int n = 8, off = 16; n >= 1; n >>= 1, off >>= 1) {
+                for (int n = 4, off = 16; n >= 1; n >>= 1, off >>= 1) {
                     const bool up = lane & off;
 #pragma unroll
                     for (int h = 0; h < n; ++h) {
@@ -533,15 +570,16 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                         sum[h] = keep + __shfl_xor_sync(0xffffffffu, give, off);
                     }
                 }
+                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
                 sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-                // lane bits 4..1 chose heads' bits 3..0
+                // lane bits 4..2 chose heads' bits 2..0
                 wait(B_L_EMPTY + (c.m & 1), ((c.m >> 1) & 1) ^ 1);
                 __syncwarp();
-                if ((lane & 1) == 0)
-                    reinterpret_cast<float*>(smem + OFF_SUM)[((c.m & 1) * SWARPS + warp) * H + (lane >> 1)] = sum[0];
-                if (tid == 0)
+                if ((lane & 3) == 0)
+                    reinterpret_cast<float*>(smem + OFF_SUM)[((c.m & 1) * 4 + qd) * H + hg * HG + (lane >> 2)] = sum[0];
+                if (qd == 0 && lane == 0)
 #pragma unroll
-                    for (int h = 0; h < H; ++h) reinterpret_cast<float*>(smem + OFF_REF)[(c.m & 1) * H + h] = ref[h];
+                    for (int h = 0; h < HG; ++h) reinterpret_cast<float*>(smem + OFF_REF)[(c.m & 1) * H + hg * HG + h] = ref[h];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_L_FULL + (c.m & 1)));
             }
@@ -551,90 +589,83 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         const int ew = warp - EWARP0, et = tid - EWARP0 * 32;
         const int qh = et / 8, ql = et % 8;                  // this thread's head, and its eighth
         const uint32_t lanes = (uint32_t)(32 * ew) << 16;
-        uint4 qv[9];
-        auto load_q = [&](const Cursor& cu) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)cu.tr.i * H + qh) * DQK);
+        bool have = false;                                   // an item whose output is to come
+        int om = 0, oi = 0, oidx = 0;                        // its number, its token, its index
+        for (;;) {
+            if (c.valid) {
+                // The terms of the next item's queries into shared memory, once the last S of
+                // the item before has read its own; and the heads' logit factors.
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)c.it.i * H + qh) * DQK);
+                uint4 qv[9];
+                __half2 top2 = __float2half2_rn(0.f);
 #pragma unroll
-            for (int k = 0; k < 9; ++k) qv[k] = __ldg(src + 8 * k + ql);
-        };
-        // The terms of item m's queries into shared memory, and the heads' logit factors.
-        auto store_q = [&](int m) {
-            float top = 0.f;
+                for (int k = 0; k < 9; ++k) qv[k] = __ldg(src + 8 * k + ql);
 #pragma unroll
-            for (int k = 0; k < 9; ++k) {
-                const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+                for (int k = 0; k < 9; ++k) {
+                    const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
-                    if (fabsf(f.x) < INFINITY) top = fmaxf(top, fabsf(f.x));
-                    if (fabsf(f.y) < INFINITY) top = fmaxf(top, fabsf(f.y));
+                    for (int x = 0; x < 4; ++x) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&u[x])));
                 }
-            }
+                float top = fminf(fmaxf(__low2float(top2), __high2float(top2)), 65504.f);
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const int e = scale_exponent(top);
-            const float up = pow2f(-e);
-            if (ql == 0) reinterpret_cast<float*>(smem + OFF_QS)[(m & 3) * H + qh] = pow2f(e) * p.scale_log2;
+                for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const int e = max(scale_exponent(top), -30);         // 2^30 is two fp16 factors
+                const __half2 up0 = __float2half2_rn(pow2f(-e / 2)), up1 = __float2half2_rn(pow2f(-e - -e / 2));
+                uint32_t w[9][QT][2];
 #pragma unroll
-            for (int k = 0; k < 9; ++k) {
-                const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-                float v[8];
+                for (int k = 0; k < 9; ++k) {
+                    const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[x]));
-                    v[2 * x] = fmaf(f.x * up, 0.f, f.x * up);        // an infinity becomes NaN
-                    v[2 * x + 1] = fmaf(f.y * up, 0.f, f.y * up);
-                }
+                    for (int x = 0; x < 4; ++x) {
+                        __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u[x]), up0), up1);
+                        v = __hfma2(v, __float2half2_rn(0.f), v);    // an infinity becomes NaN
 #pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    uint32_t w[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        w[x] = e4m3x4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                        if (t + 1 < QT) {
-                            const float2 lo = __half22float2(e4m3x2_half2(w[x] & 0xffffu));
-                            const float2 hi = __half22float2(e4m3x2_half2(w[x] >> 16));
-                            v[4 * x] = (v[4 * x] - lo.x) * 16.f;
-                            v[4 * x + 1] = (v[4 * x + 1] - lo.y) * 16.f;
-                            v[4 * x + 2] = (v[4 * x + 2] - hi.x) * 16.f;
-                            v[4 * x + 3] = (v[4 * x + 3] - hi.y) * 16.f;
+                        for (int t = 0; t < QT; ++t) {
+                            const uint32_t two = e4m3x2_of(v);
+                            if (t + 1 < QT) v = left16(v, two);
+                            w[k][t][x / 2] = x & 1 ? __byte_perm(w[k][t][x / 2], two, 0x5410) : two;
                         }
                     }
-                    // dims 64k + 8ql ..: half a 16-byte chunk of row t * 16 + qh
-                    const int row = t * H + qh, ch = 4 * (k & 1) + ql / 2;
-                    uint8_t* at = k < 8 ? smem + OFF_Q + (k / 2) * QSLAB + row * 128 + ((ch ^ (row & 7)) << 4)
-                                        : smem + OFF_Q + TILES * QSLAB + row * 64 + (((ql / 2) ^ ((row >> 1) & 3)) << 4);
-                    *reinterpret_cast<uint2*>(at + 8 * (ql & 1)) = make_uint2(w[0], w[1]);
                 }
+                if (have && !__all_sync(0xffffffffu, wait(B_Q_EMPTY, om & 1))) break;
+                if (ql == 0) reinterpret_cast<float*>(smem + OFF_QS)[(c.m & 3) * H + qh] = pow2f(e) * p.scale_log2;
+                // dims 64k + 8ql ..: half a 16-byte chunk of row t * 16 + qh (whose swizzles are
+                // qh's, t * 16 being whole atoms)
+                uint8_t* at[2] = {smem + OFF_Q + qh * 128 + (((ql / 2) ^ (qh & 7)) << 4) + 8 * (ql & 1),
+                                  smem + OFF_Q + qh * 128 + (((4 + ql / 2) ^ (qh & 7)) << 4) + 8 * (ql & 1)};
+                uint8_t* last = smem + OFF_Q + TILES * QSLAB + qh * 64 + (((ql / 2) ^ ((qh >> 1) & 3)) << 4) + 8 * (ql & 1);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint2*>(at[k & 1] + (k / 2) * QSLAB + t * H * 128) = make_uint2(w[k][t][0], w[k][t][1]);
+                    *reinterpret_cast<uint2*>(last + t * H * 64) = make_uint2(w[8][t][0], w[8][t][1]);
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_Q_FULL));
             }
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_Q_FULL));
-        };
-        if (c.valid) {
-            load_q(c);
-            store_q(0);
-        }
-        while (c.valid) {
-            const Cursor it = c;
-            c.next_item(p);
-            if (c.valid) {
-                load_q(c);
-                if (!__all_sync(0xffffffffu, wait(B_Q_EMPTY, it.m & 1))) break;   // the last S has read it
-                store_q(c.m);
-            }
-            const bool ok = wait(B_L_FULL + (it.m & 1), (it.m >> 1) & 1) && wait(B_O_FULL, it.m & 1);
+            if (!have && !c.valid) break;
+            const bool output = have;
+            const int m = om, oi_ = oi, oidx_ = oidx;
+            have = c.valid;
+            om = c.m;
+            oi = c.it.i;
+            oidx = c.idx;
+            if (c.valid) c.next_item(p);
+            if (!output) continue;
+            const bool ok = wait(B_L_FULL + (m & 1), (m >> 1) & 1) && wait(B_O_FULL, m & 1);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const float* sums = reinterpret_cast<const float*>(smem + OFF_SUM) + (it.m & 1) * SWARPS * H;
+            const float* sums = reinterpret_cast<const float*>(smem + OFF_SUM) + (m & 1) * 4 * H;
             const int hl = lane & 15;
             const float L = (sums[hl] + sums[H + hl]) + (sums[2 * H + hl] + sums[3 * H + hl]);
-            const float ref = reinterpret_cast<const float*>(smem + OFF_REF)[(it.m & 1) * H + hl];
+            const float ref = reinterpret_cast<const float*>(smem + OFF_REF)[(m & 1) * H + hl];
             const float mul = p.split ? 1.f : L > 0.f || !(L == L) ? 1.f / L : 0.f;
-            float* out = p.split ? p.part_o + (size_t)it.tr.item * H * DV : p.out + (size_t)it.tr.i * H * DV;
+            float* out = p.split ? p.part_o + (size_t)oidx_ * H * DV : p.out + (size_t)oi_ * H * DV;
             if (p.split && ew == 0 && lane < H) {
-                p.part_ml[(size_t)it.tr.item * 2 * H + hl] = ref;
-                p.part_ml[(size_t)it.tr.item * 2 * H + H + hl] = L;
+                p.part_ml[(size_t)oidx_ * 2 * H + hl] = ref;
+                p.part_ml[(size_t)oidx_ * 2 * H + H + hl] = L;
             }
 #pragma unroll 1
             for (int t = 0; t < TILES; ++t) {
@@ -649,7 +680,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(B_O_EMPTY));
-                        mbar_arrive(bar(B_L_EMPTY + (it.m & 1)));
+                        mbar_arrive(bar(B_L_EMPTY + (m & 1)));
                     }
                 }
 #pragma unroll
@@ -666,7 +697,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == MWARP) tmem_dealloc(tmem, 512);
+    if (warp == SMMA) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace ds4sp
