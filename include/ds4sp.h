@@ -114,8 +114,8 @@ typedef struct {
                             stores them (ds4sp_cache_bytes(5, 576, rows) bytes): the
                             attention multiplies the e4m3 codes as they are, on the
                             tcgen05 tensor cores, with the queries and the probabilities
-                            as sums of e4m3 terms (pv_mode 0: three terms of P, about 12
-                            bits; 1: five, about 20); it needs exp_mode 0 and attn_kernel
+                            as sums of e4m3 terms (pv_mode 0: three terms, fp16
+                            probabilities; 1: five, about 20 bits); it needs exp_mode 0 and attn_kernel
                             0. Other values are DS4SP_ERR_INVALID_ARG
                             ("Q4_0 K/V cache" and "Q8 K / Q4 V", "perf(ds4): extend sparse
                             prefill scheduling to 10K", Production workflow and the

@@ -149,7 +149,7 @@ __device__ __noinline__ bool mbar_wait_out_of_line(uint32_t bar, uint32_t parity
 }
 __device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, const WaitCtl& w, bool& abort) {
     if (abort) return false;
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_test_wait(bar, parity)) return true;
     abort = !mbar_wait_out_of_line(bar, parity, w);
     return !abort;
 }

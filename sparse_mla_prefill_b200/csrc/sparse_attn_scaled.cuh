@@ -15,10 +15,10 @@
 //   O^T = codes^T . [b0 .. b_{NT-1}]         M = 128 value dims x 4, N = NT x 16, K = rows
 //   out = O / sum(w / s_r)
 //
-// NT = 5 carries w to 2^-20 (pv_mode 1: the result is right to fp32 sums), NT = 3 to 2^-12
-// (pv_mode 0: as fp16 probabilities). Each rounding to e4m3 is of what the terms before it
-// left, so the terms' sum is w but for the last one's rounding, and products of e4m3 values
-// are exact in the fp32 accumulator.
+// w is split as hi + lo, hi its fp16 rounding: three terms hold hi (NT = 3, pv_mode 0: fp16
+// probabilities), two more lo to 2^-20 of w (NT = 5, pv_mode 1: the result is right to fp32
+// sums). Each rounding to e4m3 is of what the terms before it left, so nothing is lost but the
+// last one's remainder, and products of e4m3 values are exact in the fp32 accumulator.
 //
 // What bounds it: each unit's rows pass through the tensor cores twice, from shared memory.
 // An M = 128, K = 32 instruction takes about 50 cycles whatever N up to 80 (measured: its
@@ -87,13 +87,20 @@ static_assert(SMEM_BYTES <= attn::SMEM_LIMIT, "shared memory budget");
 // TMEM columns: two S accumulators, then the four tiles of O^T.
 constexpr int TM_S = 0, TM_O = 2 * QROWS;
 template <int NT> constexpr int o_cols() { return NT * H; }
+// The columns' order: term t of heads 8g .. 8g+7 (softmax group g) starts at o_col(g, t), so
+// that a thread's terms are 16-byte chunks: pairs of terms, and the last one beside the other
+// group's.
+template <int NT>
+__host__ __device__ constexpr int o_col(int g, int t) {
+    return t + 1 < NT ? (g * (NT - 1) / 2 + t / 2) * H + t % 2 * HG : (NT - 1) * H + g * HG;
+}
 static_assert(TM_O + TILES * o_cols<5>() <= 512, "TMEM columns");
 
 // Shared-memory descriptors (start address added): K-major rows of 128 bytes (8-row groups
 // 1024 bytes apart, 128-byte swizzle) or of 64 bytes (512 apart, 64-byte swizzle); the same
 // 128-byte atoms read with the dims as M (8-row groups are then steps along K); and P, with
-// no swizzle: 16 heads x 8 rows of 128 bytes, row groups 128 bytes apart along K, terms
-// 2048 bytes apart along N.
+// no swizzle: 16 columns x 8 rows of 128 bytes, row groups 128 bytes apart along K, the next
+// 16 columns 2048 bytes apart along N.
 __host__ __device__ constexpr uint64_t desc_bits(uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
     return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | (uint64_t)swizzle << 61;
 }
@@ -154,11 +161,6 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void regs_after_wait(uint32_t (&r)[8]) {
     asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 }
-__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[16]) {
-    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                      "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
 __device__ __forceinline__ float warp_max(float v) {         // NaNs are ignored
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             const bool first = c.u == 0;
             wait(B_ROPE_FULL + rope, rope_phase);
             const float sv = scales[rope * M + r];
+            wait(B_P_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1);   // O^T of the unit before last: its weights
             wait(B_S_FULL + (g & 1), (g >> 1) & 1);
             __syncwarp();
             tc_fence_after();
@@ -513,7 +516,8 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int col = hg * HG; col < TILES * OC; col += H) {
+                    for (int i = 0; i < TILES * NT; ++i) {
+                        const int col = i / NT * OC + o_col<NT>(hg, i % NT);
                         uint32_t o[8];
                         tmem_ld_x8(tmem + lanes + TM_O + col, o);
                         tmem_ld_wait();
@@ -533,8 +537,8 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 acc[h] = w;
                 sum[h] = fmaf(w, inv, sum[h]);
             }
-            // w = hi + lo, two fp16 values: three terms hold hi, and two more (NT = 5) what it
-            // leaves, times 16^3.
+            // w = hi + lo, two fp16 values: three terms of hi, and (NT = 5) two more of what they
+            // leave, of a small hi, and lo, times 16^3.
             uint32_t codes[NT][2];
 #pragma unroll
             for (int q = 0; q < HG / 2; ++q) {
@@ -543,18 +547,20 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 const float2 hi = __half22float2(v);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    if (t == 3) v = __floats2half2_rn((acc[2 * q] - hi.x) * 4096.f, (acc[2 * q + 1] - hi.y) * 4096.f);
+                    if (t == 3)
+                        v = __hadd2(v, __floats2half2_rn((acc[2 * q] - hi.x) * 4096.f, (acc[2 * q + 1] - hi.y) * 4096.f));
                     tc[t] = e4m3x2_of(v);
-                    if (t != 2 && t + 1 < NT) v = left16(v, tc[t]);
+                    if (t + 1 < NT) v = left16(v, tc[t]);
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) codes[t][q / 2] = q & 1 ? __byte_perm(codes[t][q / 2], tc[t], 0x5410) : tc[t];
             }
-            wait(B_P_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1);   // O^T of the unit before last
-            __syncwarp();
-            uint8_t* prow = smem + OFF_P + (g & 1) * PBUF + r * H + hg * HG;
+            const uint32_t prow = base + OFF_P + (g & 1) * PBUF + r * H + hg * (NT - 1) / 2 * (M * H);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) *reinterpret_cast<uint2*>(prow + t * (M * H)) = make_uint2(codes[t][0], codes[t][1]);
+            for (int t = 0; t + 1 < NT; t += 2)
+                st_shared_v4(prow + t / 2 * (M * H), make_uint4(codes[t][0], codes[t][1], codes[t + 1][0], codes[t + 1][1]));
+            *reinterpret_cast<uint2*>(smem + OFF_P + (g & 1) * PBUF + r * H + (NT - 1) * (M * H) + hg * HG) =
+                make_uint2(codes[NT - 1][0], codes[NT - 1][1]);
             fence_async_proxy();
             tc_fence_before();
             __syncwarp();
@@ -596,15 +602,20 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 // The terms of the next item's queries into shared memory, once the last S of
                 // the item before has read its own; and the heads' logit factors.
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)c.it.i * H + qh) * DQK);
-                uint4 qv[9];
+                // (two passes over the head's values, the second from cache: its largest, then
+                // the terms, which wait in registers)
                 __half2 top2 = __float2half2_rn(0.f);
+#pragma unroll 1
+                for (int k3 = 0; k3 < 9; k3 += 3) {
+                    uint4 qv[3];
 #pragma unroll
-                for (int k = 0; k < 9; ++k) qv[k] = __ldg(src + 8 * k + ql);
+                    for (int k = 0; k < 3; ++k) qv[k] = __ldg(src + 8 * (k3 + k) + ql);
 #pragma unroll
-                for (int k = 0; k < 9; ++k) {
-                    const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&u[x])));
+                        for (int x = 0; x < 4; ++x) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&u[x])));
+                    }
                 }
                 float top = fminf(fmaxf(__low2float(top2), __high2float(top2)), 65504.f);
 #pragma unroll
@@ -614,7 +625,8 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 uint32_t w[9][QT][2];
 #pragma unroll
                 for (int k = 0; k < 9; ++k) {
-                    const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+                    const uint4 qv = __ldg(src + 8 * (k < 8 ? k ^ (qh & 1) : k) + ql);
+                    const uint32_t u[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u[x]), up0), up1);
@@ -630,9 +642,12 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 if (have && !__all_sync(0xffffffffu, wait(B_Q_EMPTY, om & 1))) break;
                 if (ql == 0) reinterpret_cast<float*>(smem + OFF_QS)[(c.m & 3) * H + qh] = pow2f(e) * p.scale_log2;
                 // dims 64k + 8ql ..: half a 16-byte chunk of row t * 16 + qh (whose swizzles are
-                // qh's, t * 16 being whole atoms)
-                uint8_t* at[2] = {smem + OFF_Q + qh * 128 + (((ql / 2) ^ (qh & 7)) << 4) + 8 * (ql & 1),
-                                  smem + OFF_Q + qh * 128 + (((4 + ql / 2) ^ (qh & 7)) << 4) + 8 * (ql & 1)};
+                // qh's, t * 16 being whole atoms). Odd heads take k ^ 1, so that a warp's four
+                // heads cover both halves of the banks.
+                uint8_t* at[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    at[k] = smem + OFF_Q + qh * 128 + (((4 * (k ^ (qh & 1)) + ql / 2) ^ (qh & 7)) << 4) + 8 * (ql & 1);
                 uint8_t* last = smem + OFF_Q + TILES * QSLAB + qh * 64 + (((ql / 2) ^ ((qh >> 1) & 3)) << 4) + 8 * (ql & 1);
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
@@ -667,15 +682,17 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 p.part_ml[(size_t)oidx_ * 2 * H + hl] = ref;
                 p.part_ml[(size_t)oidx_ * 2 * H + H + hl] = L;
             }
+            // Eight heads of a tile at a time.
 #pragma unroll 1
-            for (int t = 0; t < TILES; ++t) {
-                uint32_t o[NT][16];
+            for (int part = 0; part < 2 * TILES; ++part) {
+                const int t = part >> 1, h0 = (part & 1) * HG;
+                uint32_t o[NT][8];
 #pragma unroll
-                for (int k = 0; k < NT; ++k) tmem_ld_x16(tmem + lanes + TM_O + t * OC + k * H, o[k]);
+                for (int k = 0; k < NT; ++k) tmem_ld_x8(tmem + lanes + TM_O + t * OC + o_col<NT>(part & 1, k), o[k]);
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < NT; ++k) regs_after_wait(o[k]);
-                if (t + 1 == TILES) {                        // O^T and the sums are read
+                if (part + 1 == 2 * TILES) {                 // O^T and the sums are read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -683,12 +700,13 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                         mbar_arrive(bar(B_L_EMPTY + (m & 1)));
                     }
                 }
+                float* to = out + h0 * DV + 128 * t + 32 * ew + lane;
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
+                for (int h = 0; h < HG; ++h) {
                     float v = __uint_as_float(o[NT - 1][h]);
 #pragma unroll
                     for (int k = NT - 2; k >= 0; --k) v = fmaf(v, 0.0625f, __uint_as_float(o[k][h]));
-                    out[h * DV + 128 * t + 32 * ew + lane] = v * __shfl_sync(0xffffffffu, mul, h);
+                    to[h * DV] = v * __shfl_sync(0xffffffffu, mul, h0 + h);
                 }
             }
         }

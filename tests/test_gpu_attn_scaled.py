@@ -7,10 +7,11 @@ left is fp32 sums and the terms of the probabilities. S sums 576 products in fp3
 18 instructions rounds the running sum, and the whole is off by about 2^-22 of
 sum|q k| <= |q| |k|; times scale that is a logit error of 2^-22 * |q| |k| / 24, below 2e-5
 for |q| |k| up to 2,000 (the inputs here: |q| ~ 24, |k| < 80). The exponential adds 2^-22.
-P in five terms keeps 2^-20 of a weight, in three 2^-12 (each term four bits), of random
-sign. The 640 rows' errors do not add up in phase, but the bound takes them as if they did:
-pv_mode 1 3e-5 (2e-5 + 2^-22 + 2^-20 + sums of 640 in fp32, 2^-24 * 5 instructions a unit),
-pv_mode 0 3e-5 + 2^-12 = 3e-4, each of sum p |v|, which for cancelling values is larger than
+A weight is first hi + lo, hi its fp16 rounding: pv_mode 0 keeps hi alone, off by at most
+2^-11 of the weight (its three terms of four bits hold hi's eleven); pv_mode 1 adds two terms
+of lo, which leave 2^-20. The 640 rows' errors do not add up in phase, but the bound takes
+them as if they did: pv_mode 1 3e-5 (2e-5 + 2^-22 + 2^-20 + sums of 640 in fp32, 2^-24 * 5
+instructions a unit), pv_mode 0 3e-5 + 2^-11 = 5.2e-4, each of sum p |v|, which for cancelling values is larger than
 |out|: both bounds are applied to sum p |v| per element. The last term's smallest spacing is
 2^-9 of its unit, so a row also adds up to 2^-10 / 16^(terms - 1) of |code|, in the unit of
 its weight w = p s / (p s)_max at least: over the sum of w / s this is the bound's second
@@ -25,7 +26,7 @@ from sparse_mla_prefill_b200 import build as B
 from sparse_mla_prefill_b200 import ds4sp as D
 
 pytestmark = pytest.mark.gpu
-TOL = {0: 3e-4, 1: 3e-5}
+TOL = {0: 5.2e-4, 1: 3e-5}
 FLOOR = {0: 2.0 ** -18, 1: 2.0 ** -26}
 
 
