@@ -32,8 +32,9 @@
 // Roles: warps 0-7 softmax, 8-11 the queries' terms and the output, 12-15 gather (16-byte
 // cp.async), warp 16 issues S and warp 17 O^T: an MMA of this size is short
 // against a wait's latency, and with two issuers each one's waits run under the other's MMAs.
-// The reference ref_h is the first unit's maximum and is raised (O and the sums rescaled)
-// only when a unit exceeds it by 2^8: e4m3 holds weights up to 448.
+// The reference ref_h is set 2^3 above the first unit's maximum, and raised (O and the sums
+// rescaled) only when a unit exceeds it by 2^8, e4m3 holding weights up to 448: for logits of
+// wide spread one unit in seven, against one in three with the maximum itself.
 // Every wait is bounded; a wait that gives up sets the launch's abort word and every role
 // drains.
 #pragma once
@@ -60,7 +61,9 @@ constexpr int HG = H / 2;                       // heads of a softmax group of f
 constexpr int EWARP0 = SWARPS, PWARP0 = EWARP0 + EWARPS, SMMA = PWARP0 + PWARPS, OMMA = SMMA + 1;
 constexpr int THREADS = (OMMA + 1) * 32;
 constexpr int SOFTMAX_BAR = 1;                  // and 2: one per group
-constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference
+constexpr int OUT_BAR = 3;
+constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference, which
+constexpr float START = 3.f;                    // is set so many above a unit's maximum
 
 constexpr int OFF_SLAB = 0;
 constexpr int OFF_ROPE = OFF_SLAB + SLOTS * SLAB;
@@ -68,9 +71,9 @@ constexpr int OFF_Q = OFF_ROPE + ROPES * ROPE;
 constexpr int OFF_P = OFF_Q + QBYTES;                        // two buffers of NT x 128 rows x 16 bytes
 constexpr int OFF_SCALE = OFF_P + 2 * 5 * M * H;             // rows' scales, one array per rope slot
 constexpr int OFF_QS = OFF_SCALE + ROPES * M * 4;            // heads' logit factors, four tokens
-constexpr int OFF_RED = OFF_QS + 4 * H * 4;                  // per warp of a group: maxima
-constexpr int OFF_SUM = OFF_RED + 4 * H * 4;                 // per warp of a group: sums, two tokens
-constexpr int OFF_REF = OFF_SUM + 2 * 4 * H * 4;             // references, two tokens
+constexpr int OFF_RED = OFF_QS + 4 * H * 4;                  // maxima per lane quarter, two units
+constexpr int OFF_SUM = OFF_RED + 2 * 4 * H * 4;             // sums per lane quarter
+constexpr int OFF_REF = OFF_SUM + 4 * H * 4;                 // references, two tokens
 constexpr int OFF_BAR = OFF_REF + 2 * H * 4;
 // barriers
 constexpr int B_SLAB_FULL = 0, B_SLAB_EMPTY = B_SLAB_FULL + SLOTS, B_ROPE_FULL = B_SLAB_EMPTY + SLOTS,
@@ -84,8 +87,9 @@ static_assert(OFF_ROPE % 1024 == 0 && OFF_Q % 1024 == 0 && QSLAB % 1024 == 0 && 
               "swizzle atoms and barriers aligned");
 static_assert(SMEM_BYTES <= attn::SMEM_LIMIT, "shared memory budget");
 
-// TMEM columns: two S accumulators, then the four tiles of O^T.
-constexpr int TM_S = 0, TM_O = 2 * QROWS;
+// TMEM columns: two S accumulators, the four tiles of O^T, and each row's share of the heads'
+// sums (two tokens).
+constexpr int TM_S = 0, TM_O = 2 * QROWS, TM_SUM = 480;
 template <int NT> constexpr int o_cols() { return NT * H; }
 // The columns' order: term t of heads 8g .. 8g+7 (softmax group g) starts at o_col(g, t), so
 // that a thread's terms are 16-byte chunks: pairs of terms, and the last one beside the other
@@ -94,7 +98,7 @@ template <int NT>
 __host__ __device__ constexpr int o_col(int g, int t) {
     return t + 1 < NT ? (g * (NT - 1) / 2 + t / 2) * H + t % 2 * HG : (NT - 1) * H + g * HG;
 }
-static_assert(TM_O + TILES * o_cols<5>() <= 512, "TMEM columns");
+static_assert(TM_O + TILES * o_cols<5>() <= TM_SUM && TM_SUM + 2 * H <= 512, "TMEM columns");
 
 // Shared-memory descriptors (start address added): K-major rows of 128 bytes (8-row groups
 // 1024 bytes apart, 128-byte swizzle) or of 64 bytes (512 apart, 64-byte swizzle); the same
@@ -169,23 +173,34 @@ __device__ __forceinline__ float warp_max(float v) {         // NaNs are ignored
 
 // A work item: a token's rows, or in split mode (few tokens) 32 of them. Row r of the item
 // is a selected compressed row for r < nsel, then window row s_lo + r - nsel.
+constexpr int RATIO = 4;       // raw tokens per compressed row (the one ratio a handle takes)
 struct Item {
     int i, t, nv;              // token of the call, absolute token, compressed rows it sees
     int nsel, s_lo;
     int row0, rows;            // the item's rows among the token's, [row0, row0 + rows)
+    __device__ __forceinline__ void of_token(const AttnParams& p, int token) {
+        i = token;
+        t = p.t0 + token;
+        nv = (t + 1) / RATIO;
+        nsel = min(p.k, nv);
+        s_lo = max(0, t - p.n_swa + 1);
+        row0 = 0;
+        rows = nsel + t - s_lo + 1;
+    }
 };
 
-// Out of line: every role walks the items, and takes one per token.
-__device__ __noinline__ Item take_item(const AttnParams& p, int idx) {
-    const TokenRows tr = token_rows(p, idx);
+// Split mode: items are the 32-row units of token 0, then token 1, ... (out of line: one item
+// per CTA).
+__device__ __noinline__ Item split_item(const AttnParams& p, int idx) {
     Item it;
-    it.i = tr.i;
-    it.t = tr.t;
-    it.nv = tr.nv;
-    it.nsel = tr.nsel;
-    it.s_lo = tr.s_lo;
-    it.row0 = p.split ? SPLIT_ROWS * tr.u0 : 0;
-    it.rows = p.split ? min(SPLIT_ROWS, tr.nrows - it.row0) : tr.nrows;
+    for (int i = 0;; ++i) {
+        it.of_token(p, i);
+        const int units = (it.rows + SPLIT_ROWS - 1) / SPLIT_ROWS;
+        if (idx < units || i + 1 >= p.n_q) break;
+        idx -= units;
+    }
+    it.row0 = SPLIT_ROWS * idx;
+    it.rows = min(SPLIT_ROWS, it.rows - it.row0);
     return it;
 }
 
@@ -197,7 +212,9 @@ struct Cursor {
     __device__ __forceinline__ void take(const AttnParams& p) {
         valid = idx < p.n_items;
         u = 0;
-        if (valid) it = take_item(p, idx);
+        if (!valid) return;
+        if (p.split) it = split_item(p, idx);
+        else it.of_token(p, p.n_q - 1 - idx);                // heaviest (latest) first
     }
     __device__ __forceinline__ void start(const AttnParams& p) {
         m = 0;
@@ -437,19 +454,17 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         const uint32_t lanes = (uint32_t)(32 * qd) << 16;    // the warp's TMEM lanes
         const float* scales = reinterpret_cast<const float*>(smem + OFF_SCALE);
         const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + hg * HG;
-        float* red = reinterpret_cast<float*>(smem + OFF_RED) + hg * HG;
         const int group_bar = SOFTMAX_BAR + hg;
         float ref[HG], sum[HG], cq[HG];
         int rope = 0;
-        uint32_t rope_phase = 0;
         for (int g = 0; c.valid; ++g, c.advance(p)) {
             const bool first = c.u == 0;
-            wait(B_ROPE_FULL + rope, rope_phase);
-            const float sv = scales[rope * M + r];
             wait(B_P_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1);   // O^T of the unit before last: its weights
             wait(B_S_FULL + (g & 1), (g >> 1) & 1);
             __syncwarp();
             tc_fence_after();
+            // (S was issued after its issuer saw the unit's rows, and scales, arrive.)
+            const float sv = scales[rope * M + r];
             float acc[HG];
             {
                 uint32_t d0[8], d1[8], d2[8];
@@ -479,10 +494,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 mbar_arrive(bar(B_S_EMPTY + (g & 1)));
                 mbar_arrive(bar(B_ROPE_EMPTY + rope));
             }
-            if (++rope == ROPES) {
-                rope = 0;
-                rope_phase ^= 1;
-            }
+            if (++rope == ROPES) rope = 0;
             const bool valid = sv > 0.f;
             const int sexp = (int)(__float_as_uint(sv) >> 23) - 127;
             const float lsv = (float)sexp;                   // log2 of the row's scale
@@ -492,21 +504,22 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 acc[h] = fmaf(acc[h], cq[h] * sv, lsv);      // log2 of the row's weight
                 top = fmaxf(top, acc[h] - ref[h]);
             }
-            if (named_barrier_or(group_bar, 128, first || abort || (valid && top > HEADROOM))) {
+            if (first || named_barrier_or(group_bar, 128, abort || (valid && top > HEADROOM))) {
                 // A new reference: the first unit's maximum, or one raised by this unit.
-                if (named_barrier_or(group_bar, 128, abort)) break;
+                float* red = reinterpret_cast<float*>(smem + OFF_RED) + ((g & 1) * H + hg * HG) * 4;   // [head][quarter]
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
                     const float mx = warp_max(valid ? acc[h] : -INFINITY);
-                    if (lane == 0) red[qd * H + h] = mx;
+                    if (lane == 0) red[4 * h + qd] = mx;
                 }
-                named_barrier(group_bar, 128);
+                if (named_barrier_or(group_bar, 128, abort)) break;
                 float alpha[HG];
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
-                    const float mu = fmaxf(fmaxf(red[h], red[H + h]), fmaxf(red[2 * H + h], red[3 * H + h]));
-                    const float was = first ? (mu > -INFINITY ? mu : 0.f) : ref[h];
-                    ref[h] = mu > was + HEADROOM ? mu : was;
+                    const float4 m4 = *reinterpret_cast<const float4*>(red + 4 * h);
+                    const float mu = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                    const float was = first ? (mu > -INFINITY ? mu + START : 0.f) : ref[h];
+                    ref[h] = mu > was + HEADROOM ? mu + START : was;
                     alpha[h] = fast_exp2(was - ref[h]);
                     sum[h] *= alpha[h];
                 }
@@ -516,15 +529,19 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int i = 0; i < TILES * NT; ++i) {
-                        const int col = i / NT * OC + o_col<NT>(hg, i % NT);
-                        uint32_t o[8];
-                        tmem_ld_x8(tmem + lanes + TM_O + col, o);
-                        tmem_ld_wait();
-                        regs_after_wait(o);
+                    for (int t = 0; t < TILES; ++t) {
+                        const uint32_t at = tmem + lanes + TM_O + t * OC;
+                        uint32_t o[NT][8];
 #pragma unroll
-                        for (int h = 0; h < HG; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
-                        tmem_st_x8(tmem + lanes + TM_O + col, o);
+                        for (int k = 0; k < NT; ++k) tmem_ld_x8(at + o_col<NT>(hg, k), o[k]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) {
+                            regs_after_wait(o[k]);
+#pragma unroll
+                            for (int h = 0; h < HG; ++h) o[k][h] = __float_as_uint(__uint_as_float(o[k][h]) * alpha[h]);
+                            tmem_st_x8(at + o_col<NT>(hg, k), o[k]);
+                        }
                     }
                     tmem_st_wait();
                 }
@@ -566,26 +583,18 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_P_FULL + (g & 1)));
             if (c.last()) {
-                // The item's sums: eight heads over 32 lanes, halving the heads a lane holds.
-#pragma unroll
-                for (int n = 4, off = 16; n >= 1; n >>= 1, off >>= 1) {
-                    const bool up = lane & off;
-#pragma unroll
-                    for (int h = 0; h < n; ++h) {
-                        const float give = up ? sum[h] : sum[h + n], keep = up ? sum[h + n] : sum[h];
-                        sum[h] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                    }
-                }
-                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
-                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-                // lane bits 4..2 chose heads' bits 2..0
+                // The row's share of the item's sums, for the output warps to add.
                 wait(B_L_EMPTY + (c.m & 1), ((c.m >> 1) & 1) ^ 1);
                 __syncwarp();
-                if ((lane & 3) == 0)
-                    reinterpret_cast<float*>(smem + OFF_SUM)[((c.m & 1) * 4 + qd) * H + hg * HG + (lane >> 2)] = sum[0];
-                if (qd == 0 && lane == 0)
+                uint32_t bits[8];
+#pragma unroll
+                for (int h = 0; h < HG; ++h) bits[h] = __float_as_uint(sum[h]);
+                tmem_st_x8(tmem + lanes + TM_SUM + (c.m & 1) * H + hg * HG, bits);
+                if (p.split && qd == 0 && lane == 0)
 #pragma unroll
                     for (int h = 0; h < HG; ++h) reinterpret_cast<float*>(smem + OFF_REF)[(c.m & 1) * H + hg * HG + h] = ref[h];
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_L_FULL + (c.m & 1)));
             }
@@ -639,7 +648,8 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                         }
                     }
                 }
-                if (have && !__all_sync(0xffffffffu, wait(B_Q_EMPTY, om & 1))) break;
+                if (have) wait(B_Q_EMPTY, om & 1);           // (a wait that gave up: all stop below)
+                __syncwarp();
                 if (ql == 0) reinterpret_cast<float*>(smem + OFF_QS)[(c.m & 3) * H + qh] = pow2f(e) * p.scale_log2;
                 // dims 64k + 8ql ..: half a 16-byte chunk of row t * 16 + qh (whose swizzles are
                 // qh's, t * 16 being whole atoms). Odd heads take k ^ 1, so that a warp's four
@@ -669,12 +679,40 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             oidx = c.idx;
             if (c.valid) c.next_item(p);
             if (!output) continue;
-            const bool ok = wait(B_L_FULL + (m & 1), (m >> 1) & 1) && wait(B_O_FULL, m & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            wait(B_L_FULL + (m & 1), (m >> 1) & 1);
+            __syncwarp();
             tc_fence_after();
-            const float* sums = reinterpret_cast<const float*>(smem + OFF_SUM) + (m & 1) * 4 * H;
+            // The sums: 16 heads over the quarter's 32 rows, halving the heads a lane holds;
+            // then the four quarters.
+            float sum[H];
+            {
+                uint32_t bits[16];
+                tmem_ld_x16(tmem + lanes + TM_SUM + (m & 1) * H, bits);
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    asm volatile("" : "+r"(bits[h]));        // after the wait
+                    sum[h] = __uint_as_float(bits[h]);
+                }
+            }
+#pragma unroll
+            for (int n = 8, off = 16; n >= 1; n >>= 1, off >>= 1) {
+                const bool up = lane & off;
+#pragma unroll
+                for (int h = 0; h < n; ++h) {
+                    const float give = up ? sum[h] : sum[h + n], keep = up ? sum[h + n] : sum[h];
+                    sum[h] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                }
+            }
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+            float* sums = reinterpret_cast<float*>(smem + OFF_SUM);
+            if ((lane & 1) == 0) sums[ew * H + (lane >> 1)] = sum[0];   // lane bits 4..1 chose heads' bits 3..0
+            wait(B_O_FULL, m & 1);
+            if (named_barrier_or(OUT_BAR, EWARPS * 32, abort)) break;
+            tc_fence_after();
             const int hl = lane & 15;
             const float L = (sums[hl] + sums[H + hl]) + (sums[2 * H + hl] + sums[3 * H + hl]);
+            named_barrier(OUT_BAR, EWARPS * 32);             // read before the next item's are written
             const float ref = reinterpret_cast<const float*>(smem + OFF_REF)[(m & 1) * H + hl];
             const float mul = p.split ? 1.f : L > 0.f || !(L == L) ? 1.f / L : 0.f;
             float* out = p.split ? p.part_o + (size_t)oidx_ * H * DV : p.out + (size_t)oi_ * H * DV;
