@@ -887,9 +887,34 @@ ds4sp_status check_elem_ptr(const void* p, int elem, const char* name) {
     return DS4SP_OK;
 }
 
-// The kernel's table for a rotary configuration: each pair's frequency in turns, as a
-// fraction of 2^64 (the frequency itself in 64-bit floating point).
+ds4sp_status make_rope_table(const ds4sp_rope_config* cfg, RopeTable* tab);
+
+// The kernel's table for a rotary configuration. A program's configurations are few, and a
+// table costs more host time than the rest of a call: each host thread keeps its last one, by
+// the configuration's values.
 ds4sp_status rope_table(const ds4sp_rope_config* cfg, int transpose, RopeTable* tab) {
+    thread_local ds4sp_rope_config last_cfg;
+    thread_local RopeTable last;
+    thread_local bool have = false;
+    auto same = [](const ds4sp_rope_config& a, const ds4sp_rope_config& b) {
+        return a.dims == b.dims && a.offset == b.offset && a.layout == b.layout && a.scaling == b.scaling &&
+               a.base == b.base && a.factor == b.factor && a.orig_len == b.orig_len && a.beta_fast == b.beta_fast &&
+               a.beta_slow == b.beta_slow && a.mscale == b.mscale;
+    };
+    if (!cfg || !have || !same(*cfg, last_cfg)) {
+        have = false;
+        DS4SP_TRY(make_rope_table(cfg, &last));
+        last_cfg = *cfg;
+        have = true;
+    }
+    *tab = last;
+    tab->transpose = transpose != 0;
+    return DS4SP_OK;
+}
+
+// Each pair's frequency in turns, as a fraction of 2^64 (the frequency itself in 64-bit
+// floating point).
+ds4sp_status make_rope_table(const ds4sp_rope_config* cfg, RopeTable* tab) {
     if (!cfg) return fail(DS4SP_ERR_INVALID_ARG, "rope configuration is null");
     const ds4sp_rope_config& c = *cfg;
     if (c.dims < 2 || c.dims > kRopeMaxDims || c.dims % 2 || c.offset < 0)
@@ -934,38 +959,49 @@ ds4sp_status rope_table(const ds4sp_rope_config* cfg, int transpose, RopeTable* 
     tab->dims = c.dims;
     tab->offset = c.offset;
     tab->half_layout = c.layout;
-    tab->transpose = transpose != 0;
     return DS4SP_OK;
 }
 
 template <class T, int V>
-void launch_rope_v(RopeParams& p, cudaStream_t s) {
-    // Four heads a thread (cos and sin computed once for them) where that leaves every SM
-    // its threads; one head a thread for small calls, where latency counts.
-    const long long chunks = (long long)p.n * p.per_head;
-    const bool many = p.heads >= 4 && chunks * ((p.heads + 3) / 4) >= 148LL * 1024;
-    p.groups = many ? (p.heads + 3) / 4 : p.heads;
-    const unsigned grid = (unsigned)((chunks * p.groups + 255) / 256);
-    if (many)
-        rope_kernel<T, V, 4><<<grid, 256, 0, s>>>(p);
+void launch_rope_v(RopeParams& p, unsigned grid, cudaStream_t s) {
+    const size_t smem = (size_t)p.tokens * (p.tab.dims / 2) * sizeof(float2);
+    if (p.tab.half_layout)
+        rope_kernel<T, V, true><<<grid, kRopeThreads, smem, s>>>(p);
     else
-        rope_kernel<T, V, 1><<<grid, 256, 0, s>>>(p);
+        rope_kernel<T, V, false><<<grid, kRopeThreads, smem, s>>>(p);
 }
 
-void launch_rope(RopeParams& p, ds4sp_dtype t, int v, cudaStream_t s) {
-    if (t == DS4SP_F32) {
-        if (v == 4) launch_rope_v<float, 4>(p, s);
-        else if (v == 2) launch_rope_v<float, 2>(p, s);
-        else launch_rope_v<float, 1>(p, s);
-    } else if (t == DS4SP_BF16) {
-        if (v == 8) launch_rope_v<__nv_bfloat16, 8>(p, s);
-        else if (v == 2) launch_rope_v<__nv_bfloat16, 2>(p, s);
-        else launch_rope_v<__nv_bfloat16, 1>(p, s);
+template <class T>
+void launch_rope_t(RopeParams& p, int v, unsigned grid, cudaStream_t s) {
+    if (v > 2) launch_rope_v<T, 16 / sizeof(T)>(p, grid, s);
+    else if (v == 2) launch_rope_v<T, 2>(p, grid, s);
+    else launch_rope_v<T, 1>(p, grid, s);
+}
+
+// Tokens of a block: about 2,048 chunks' worth, as long as that leaves two blocks an SM (a
+// small call spreads its tokens, where latency counts); a token of more than kRopeChunks
+// chunks takes several blocks.
+ds4sp_status launch_rope(RopeParams& p, ds4sp_dtype t, int v, cudaStream_t s) {
+    const long long per_token = (long long)p.heads * p.per_head;
+    if (per_token > 0x7fffffffLL / 2)
+        return fail(DS4SP_ERR_INVALID_ARG, "%d heads of %d chunks is too many", p.heads, p.per_head);
+    p.slices = 1;
+    p.tokens = 1;
+    if (per_token > kRopeChunks) {
+        p.slices = (int)((per_token + kRopeChunks - 1) / kRopeChunks);
     } else {
-        if (v == 8) launch_rope_v<__half, 8>(p, s);
-        else if (v == 2) launch_rope_v<__half, 2>(p, s);
-        else launch_rope_v<__half, 1>(p, s);
+        const long long most = std::min<long long>(2048 / per_token, kRopeTurns / (p.tab.dims / 2));
+        p.tokens = (int)std::max<long long>(1, std::min<long long>(most, p.n / 296));
     }
+    p.by_head.set((uint32_t)p.per_head);
+    p.by_token.set((uint32_t)per_token);
+    const long long blocks = p.slices > 1 ? (long long)p.n * p.slices : (p.n + p.tokens - 1) / p.tokens;
+    if (blocks > 0x7fffffffLL) return fail(DS4SP_ERR_INVALID_ARG, "%d tokens of %d heads is too many", p.n, p.heads);
+    if (t == DS4SP_F32) launch_rope_t<float>(p, v, (unsigned)blocks, s);
+    else if (t == DS4SP_BF16) launch_rope_t<__nv_bfloat16>(p, v, (unsigned)blocks, s);
+    else launch_rope_t<__half>(p, v, (unsigned)blocks, s);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DS4SP_OK : cuda_fail(e, "rope launch");
 }
 
 // Bytes of a stored row (kv_format 5: of a place), 0 for a format or width that has none.
@@ -985,7 +1021,7 @@ void launch_cache_write_t(const CacheRows& p, const RopeTable& tab, uint8_t* cac
         case kFmtQ4: cache_write_kernel<T, kFmtQ4><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
         case kFmtQ8Q4: cache_write_kernel<T, kFmtQ8Q4><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
         default:
-            if (p.dims <= 64 * kE4M3Held)
+            if (p.dims <= 64 * kE4M3Held && p.fast)
                 cache_write_e4m3_kernel<T, true><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
             else
                 cache_write_e4m3_kernel<T, false><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
@@ -1000,8 +1036,7 @@ void launch_cache_write(const CacheRows& p, const RopeTable& tab, uint8_t* cache
 }
 
 template <class T>
-void launch_cache_read_t(const CacheRead& p, int fmt, T* out, cudaStream_t s) {
-    const unsigned grid = (unsigned)(((long long)p.n * (p.out_dims / 8) + 255) / 256);
+void launch_cache_read_t(const CacheRead& p, int fmt, unsigned grid, T* out, cudaStream_t s) {
     switch (fmt) {
         case kFmtF16: cache_read_kernel<T, kFmtF16><<<grid, 256, 0, s>>>(p, out); break;
         case kFmtQ8: cache_read_kernel<T, kFmtQ8><<<grid, 256, 0, s>>>(p, out); break;
@@ -1010,10 +1045,16 @@ void launch_cache_read_t(const CacheRead& p, int fmt, T* out, cudaStream_t s) {
     }
 }
 
-void launch_cache_read(const CacheRead& p, int fmt, void* out, ds4sp_dtype t, cudaStream_t s) {
-    if (t == DS4SP_F32) launch_cache_read_t(p, fmt, static_cast<float*>(out), s);
-    else if (t == DS4SP_BF16) launch_cache_read_t(p, fmt, static_cast<__nv_bfloat16*>(out), s);
-    else launch_cache_read_t(p, fmt, static_cast<__half*>(out), s);
+// Rows of a block: about 1,024 chunks' worth (four per thread) where that leaves four blocks
+// an SM; a small call takes a row per block.
+void launch_cache_read(CacheRead& p, int fmt, void* out, ds4sp_dtype t, cudaStream_t s) {
+    const int chunks = p.out_dims / 8;
+    p.block_rows = std::max(1, std::min(1024 / chunks, p.n / 592));
+    p.by_row.set((uint32_t)chunks);
+    const unsigned grid = (unsigned)((p.n + p.block_rows - 1) / p.block_rows);
+    if (t == DS4SP_F32) launch_cache_read_t(p, fmt, grid, static_cast<float*>(out), s);
+    else if (t == DS4SP_BF16) launch_cache_read_t(p, fmt, grid, static_cast<__nv_bfloat16*>(out), s);
+    else launch_cache_read_t(p, fmt, grid, static_cast<__half*>(out), s);
 }
 
 }  // namespace
@@ -1467,7 +1508,7 @@ ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype
     DS4SP_TRY(rope_table(cfg, transpose, &p.tab));
     const int es = dtype_bytes(dtype);
     if (es == 0) return fail(DS4SP_ERR_INVALID_ARG, "dtype %d", (int)dtype);
-    if (n_tokens < 0 || heads < 1 || head_dim < 1)
+    if (n_tokens < 0 || heads < 1 || head_dim < 1 || head_dim > kRopeMaxHead)
         return fail(DS4SP_ERR_INVALID_ARG, "n_tokens %d, heads %d, head_dim %d", n_tokens, heads, head_dim);
     if ((long long)cfg->offset + cfg->dims > head_dim)
         return fail(DS4SP_ERR_INVALID_ARG, "rotary dims [%d, %d) of a head of %d", cfg->offset,
@@ -1505,11 +1546,7 @@ ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype
     const bool in_place = x == out && x_token_stride == out_token_stride && x_head_stride == out_head_stride;
     p.rot = p.tab.half_layout ? half / v : cfg->dims / (v < 2 ? 2 : v);
     p.per_head = p.rot + (in_place ? 0 : (head_dim - cfg->dims) / v);
-    if ((double)n_tokens * heads * p.per_head > 256.0 * 0x7fffffff)
-        return fail(DS4SP_ERR_INVALID_ARG, "%d tokens of %d heads is too many", n_tokens, heads);
-    launch_rope(p, dtype, v, static_cast<cudaStream_t>(stream));
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? DS4SP_OK : cuda_fail(e, "rope launch");
+    return launch_rope(p, dtype, v, static_cast<cudaStream_t>(stream));
 }
 
 size_t ds4sp_cache_bytes(int kv_format, int dims, long long rows) {

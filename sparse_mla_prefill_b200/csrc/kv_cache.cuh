@@ -57,6 +57,54 @@ struct CacheRows {                              // the rows a write takes
                                                 // eight is partly rotated
 };
 
+template <class T>
+union Eight {
+    uint4 q[sizeof(T) / 2];
+    T e[8];
+};
+template <class T>
+__device__ __forceinline__ Eight<T> load_eight(const T* src) {          // 16-byte aligned
+    Eight<T> a;
+#pragma unroll
+    for (int w = 0; w < (int)sizeof(T) / 2; ++w) a.q[w] = __ldg(reinterpret_cast<const uint4*>(src) + w);
+    return a;
+}
+
+__device__ __forceinline__ long long position_of(const CacheRows& p, int i) {
+    return p.positions ? (long long)__ldg(p.positions + i) : p.pos0 + i * p.pos_step;
+}
+
+// Whether chunk c of eight values is rotated (p.fast: all of it or none).
+__device__ __forceinline__ bool turned(const CacheRows& p, const RopeTable& tab, int c) {
+    return p.rotate && 8 * c >= tab.offset && 8 * c < tab.offset + tab.dims;
+}
+
+// A rotated chunk c of row i, loaded as `a`, in fp32 (p.fast).
+template <class T>
+__device__ __forceinline__ void turn_eight(const CacheRows& p, const RopeTable& tab, const uint64_t* step, int i,
+                                           int c, const Eight<T>& a, float (&v)[8]) {
+    const long long pos = position_of(p, i);
+    const int r0 = 8 * c - tab.offset, half = tab.dims / 2;
+    if (tab.half_layout) {
+        const bool upper = r0 >= half;
+        const Eight<T> b = load_eight(static_cast<const T*>(p.x) + i * p.x_ld + 8 * c + (upper ? -half : half));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 cs = rope_turn(step[(upper ? r0 - half : r0) + k], pos, tab.m);
+            const float s = to_f32(a.e[k]), o = to_f32(b.e[k]);
+            v[k] = upper ? o * cs.y + s * cs.x : s * cs.x - o * cs.y;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 cs = rope_turn(step[r0 / 2 + k], pos, tab.m);
+            const float a0 = to_f32(a.e[2 * k]), b0 = to_f32(a.e[2 * k + 1]);
+            v[2 * k] = a0 * cs.x - b0 * cs.y;
+            v[2 * k + 1] = a0 * cs.y + b0 * cs.x;
+        }
+    }
+}
+
 // Eight values of row i (of the n written) at dims 8c .. 8c+7, rotated, in fp32.
 template <class T>
 __device__ __forceinline__ void load_chunk(const CacheRows& p, const RopeTable& tab, const uint64_t* step,
@@ -64,37 +112,16 @@ __device__ __forceinline__ void load_chunk(const CacheRows& p, const RopeTable& 
     const T* row = static_cast<const T*>(p.x) + i * p.x_ld;
     const int d0 = 8 * c;
     if (p.fast) {
-        union { uint4 q[sizeof(T) / 2]; T e[8]; } a, b;
-#pragma unroll
-        for (int w = 0; w < (int)sizeof(T) / 2; ++w) a.q[w] = __ldg(reinterpret_cast<const uint4*>(row + d0) + w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = to_f32(a.e[k]);
-        if (!p.rotate || d0 < tab.offset || d0 >= tab.offset + tab.dims) return;
-        const long long pos = p.positions ? (long long)__ldg(p.positions + i) : p.pos0 + i * p.pos_step;
-        const int r0 = d0 - tab.offset, half = tab.dims / 2;
-        if (tab.half_layout) {
-            const bool upper = r0 >= half;
-            const T* other = row + (upper ? d0 - half : d0 + half);
-#pragma unroll
-            for (int w = 0; w < (int)sizeof(T) / 2; ++w) b.q[w] = __ldg(reinterpret_cast<const uint4*>(other) + w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 cs = rope_turn(step[(upper ? r0 - half : r0) + k], pos, tab.m);
-                const float o = to_f32(b.e[k]);
-                v[k] = upper ? o * cs.y + v[k] * cs.x : v[k] * cs.x - o * cs.y;
-            }
+        const Eight<T> a = load_eight(row + d0);
+        if (turned(p, tab, c)) {
+            turn_eight<T>(p, tab, step, i, c, a, v);
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 cs = rope_turn(step[r0 / 2 + k], pos, tab.m);
-                const float a0 = v[2 * k], b0 = v[2 * k + 1];
-                v[2 * k] = a0 * cs.x - b0 * cs.y;
-                v[2 * k + 1] = a0 * cs.y + b0 * cs.x;
-            }
+            for (int k = 0; k < 8; ++k) v[k] = to_f32(a.e[k]);
         }
         return;
     }
-    const long long pos = !p.rotate ? 0 : p.positions ? (long long)p.positions[i] : p.pos0 + i * p.pos_step;
+    const long long pos = p.rotate ? position_of(p, i) : 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int d = d0 + k, r = d - tab.offset, half = tab.dims / 2;
@@ -230,15 +257,27 @@ __device__ __forceinline__ __half2 e4m3x2_half2(uint32_t two) {
 constexpr int kE4M3Threads = 512;               // 64 rows x 8 lanes
 constexpr int kE4M3Held = 9;                    // steps of 64 dims held in registers: up to 576 dims
 
+// The larger of `top` and the finite magnitudes of eight values.
+__device__ __forceinline__ float top_of(const float (&u)[8], float top) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float a = fabsf(u[k]);
+        if (a <= 3.402823466e38f) top = fmaxf(top, a);
+    }
+    return top;
+}
+
 // One CTA per block of 64 rows that the write touches; eight lanes a row, each taking every
-// eighth chunk of eight values. Up to 576 dims the loaded values stay in registers between
-// the block's maximum and the rounding; wider rows are loaded twice.
+// eighth chunk of eight values. HELD (up to 576 dims, aligned): the values as they were loaded
+// stay in registers between the block's maximum and the rounding, all loads in flight at once
+// (16-bit values: 64 registers, two CTAs an SM, so that one block's loads run under the
+// other's arithmetic), and only the rotated chunks are computed twice; other rows are loaded
+// twice.
 template <class T, bool HELD>
-__global__ void __launch_bounds__(kE4M3Threads)
+__global__ void __launch_bounds__(kE4M3Threads, sizeof(T) == 2 ? 2 : 1)
 cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ cache) {
     __shared__ uint64_t step[kRopeMaxDims / 2];
     __shared__ float warp_top[kE4M3Threads / 32];
-    load_steps(tab, p.rotate, step);
     const int tid = threadIdx.x, r = tid / 8, l = tid % 8;
     const int blk = p.row0 / kScaleBlock + blockIdx.x;
     const int i = blk * kScaleBlock + r - p.row0;        // this lane's row of the written ones
@@ -247,29 +286,38 @@ cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab
     uint8_t* base = cache + (long long)blk * (kScaleBlock + 1) * p.dims;
     float* record = reinterpret_cast<float*>(base + kScaleBlock * p.dims);
     const int old = blockIdx.x == 0 ? p.row0 % kScaleBlock : 0;   // rows kept from before
-    const float old_scale = old ? *record : 0.f;
-
-    float v[HELD ? kE4M3Held : 1][8];
-    float top = 0.f;
-    auto take = [&](const float (&u)[8]) {
+    Eight<T> v[HELD ? kE4M3Held : 1];
+    if constexpr (HELD)
+        if (in) {
+            const T* row = static_cast<const T*>(p.x) + i * p.x_ld;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float a = fabsf(u[k]);
-            if (a <= 3.402823466e38f) top = fmaxf(top, a);        // finite
+            for (int s = 0; s < kE4M3Held; ++s)
+                if (8 * s + l < chunks) v[s] = load_eight(row + 8 * (8 * s + l));
         }
-    };
+    const float old_scale = old ? *record : 0.f;
+    load_steps(tab, p.rotate, step);
+
+    float top = 0.f;
     if (in) {
         if constexpr (HELD) {
 #pragma unroll
-            for (int s = 0; s < kE4M3Held; ++s)
-                if (8 * s + l < chunks) {
-                    load_chunk<T>(p, tab, step, i, 8 * s + l, v[s]);
-                    take(v[s]);
+            for (int s = 0; s < kE4M3Held; ++s) {
+                const int c = 8 * s + l;
+                if (c >= chunks) continue;
+                float u[8];
+                if (turned(p, tab, c)) {
+                    turn_eight<T>(p, tab, step, i, c, v[s], u);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[k] = to_f32(v[s].e[k]);
                 }
+                top = top_of(u, top);
+            }
         } else {
             for (int c = l; c < chunks; c += 8) {
-                load_chunk<T>(p, tab, step, i, c, v[0]);
-                take(v[0]);
+                float u[8];
+                load_chunk<T>(p, tab, step, i, c, u);
+                top = top_of(u, top);
             }
         }
     }
@@ -299,8 +347,8 @@ cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab
         }
     }
     const float inv = pow2f(-e);
-    if (tid < p.dims / 4) reinterpret_cast<uint32_t*>(record)[tid] = tid == 0 ? __float_as_uint(pow2f(e)) : 0u;
-    for (int k = tid + kE4M3Threads; k < p.dims / 4; k += kE4M3Threads) reinterpret_cast<uint32_t*>(record)[k] = 0u;
+    for (int k = tid; k < p.dims / 4; k += kE4M3Threads)
+        reinterpret_cast<uint32_t*>(record)[k] = k == 0 ? __float_as_uint(pow2f(e)) : 0u;
     if (!in) return;
     auto put = [&](int c, const float (&u)[8]) {
         const uint2 w = make_uint2(e4m3x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv),
@@ -309,12 +357,23 @@ cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab
     };
     if constexpr (HELD) {
 #pragma unroll
-        for (int s = 0; s < kE4M3Held; ++s)
-            if (8 * s + l < chunks) put(8 * s + l, v[s]);
+        for (int s = 0; s < kE4M3Held; ++s) {
+            const int c = 8 * s + l;
+            if (c >= chunks) continue;
+            float u[8];
+            if (turned(p, tab, c)) {
+                turn_eight<T>(p, tab, step, i, c, v[s], u);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] = to_f32(v[s].e[k]);
+            }
+            put(c, u);
+        }
     } else {
         for (int c = l; c < chunks; c += 8) {
-            load_chunk<T>(p, tab, step, i, c, v[0]);
-            put(c, v[0]);
+            float u[8];
+            load_chunk<T>(p, tab, step, i, c, u);
+            put(c, u);
         }
     }
 }
@@ -329,70 +388,108 @@ struct CacheRead {
     int row_bytes, part_off;                    // formats 0-3: a stored row, where the part starts
     long long out_ld;                           // in values
     int fast;                                   // out's rows are 16-byte aligned
+    int block_rows;                             // rows of a block
+    SmallDiv by_row;                            // chunks of a row
 };
 
-// Eight values per thread: chunk c of row i, value = code * scale in fp32, rounded once to
-// T. An index outside the cache reads as a row of zeros.
-template <class T, int FMT>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRead p, T* __restrict__ out) {
-    const int chunks = p.out_dims / 8;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (long long)p.n * chunks) return;
-    const int i = (int)(id / chunks), c = (int)(id % chunks);
-    const int row = p.rows ? __ldg(p.rows + i) : p.row0 + i;
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.f;
-    if (row >= 0 && row < p.cache_rows) {
-        if constexpr (FMT == kFmtF16) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.cache + (long long)row * p.row_bytes + 16 * c));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-                v[2 * k] = f.x;
-                v[2 * k + 1] = f.y;
-            }
-        } else if constexpr (FMT == kFmtE4M3) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.cache + e4m3_place(row) * p.dims + 8 * c));
+// A stored chunk of eight values, and its scale.
+template <int FMT>
+struct Stored {
+    uint4 w;                                    // fp16 values, or codes in x, y
+    float scale;                                // 0: no row
+};
+template <int FMT>
+__device__ __forceinline__ Stored<FMT> load_stored(const CacheRead& p, int row, int c) {
+    Stored<FMT> s{make_uint4(0u, 0u, 0u, 0u), 0.f};
+    if (row < 0 || row >= p.cache_rows) return s;
+    if constexpr (FMT == kFmtF16) {
+        s.w = __ldg(reinterpret_cast<const uint4*>(p.cache + (long long)row * p.row_bytes + 16 * c));
+        s.scale = 1.f;
+    } else {
+        const uint8_t* codes;
+        if constexpr (FMT == kFmtE4M3) {
+            codes = p.cache + e4m3_place(row) * p.dims + 8 * c;
             const long long rec = (long long)(row / kScaleBlock) * (kScaleBlock + 1) + kScaleBlock;
-            const float s = __ldg(reinterpret_cast<const float*>(p.cache + rec * p.dims));
-            const uint32_t u[2] = {w.x, w.y};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = __half22float2(e4m3x2_half2(u[k / 2] >> (16 * (k % 2)) & 0xffffu));
-                v[2 * k] = f.x * s;
-                v[2 * k + 1] = f.y * s;
-            }
+            s.scale = __ldg(reinterpret_cast<const float*>(p.cache + rec * p.dims));
         } else {
             const uint8_t* part = p.cache + (long long)row * p.row_bytes + p.part_off;
-            const float d = __half2float(*reinterpret_cast<const __half*>(
-                part + quant_code_bytes(FMT, p.dims) + 2 * (c / 4)));
-            if constexpr (FMT == kFmtQ8) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(part + 8 * c));
-                const uint32_t u[2] = {w.x, w.y};
+            s.scale = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(
+                part + quant_code_bytes(FMT, p.dims) + 2 * (c / 4)))));
+            codes = part + (FMT == kFmtQ8 ? 8 * c : 16 * (c / 4) + 8 * (c % 2));
+        }
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes));
+        s.w.x = w.x;
+        s.w.y = w.y;
+    }
+    return s;
+}
+template <int FMT>
+__device__ __forceinline__ void values_of(const Stored<FMT>& s, int c, float (&v)[8]) {
+    const uint32_t u[4] = {s.w.x, s.w.y, s.w.z, s.w.w};
+    if constexpr (FMT == kFmtF16) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = d * (float)(int8_t)(u[k / 4] >> (8 * (k % 4)) & 0xffu);
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+            v[2 * k] = f.x;
+            v[2 * k + 1] = f.y;
+        }
+    } else if constexpr (FMT == kFmtE4M3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(e4m3x2_half2(u[k / 2] >> (16 * (k % 2)) & 0xffffu));
+            v[2 * k] = f.x * s.scale;
+            v[2 * k + 1] = f.y * s.scale;
+        }
+    } else if constexpr (FMT == kFmtQ8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = s.scale * (float)(int8_t)(u[k / 4] >> (8 * (k % 4)) & 0xffu);
+    } else {
+        const int shift = c % 4 < 2 ? 0 : 4;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = s.scale * (float)((int)(u[k / 4] >> (8 * (k % 4) + shift) & 0xfu) - 8);
+    }
+}
+
+// A block reads block_rows rows, a thread eight values at a time, four chunks in flight:
+// value = code * scale in fp32, rounded once to T. An index outside the cache reads as a row
+// of zeros.
+template <class T, int FMT>
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheRead p, T* __restrict__ out) {
+    constexpr int U = 4;
+    const int chunks = (int)p.by_row.d;
+    const int first = blockIdx.x * p.block_rows;
+    const int total = min(p.block_rows, p.n - first) * chunks;
+#pragma unroll 1
+    for (int base = threadIdx.x; base < total; base += U * 256) {
+        Stored<FMT> s[U];
+        int at[U], ch[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = base + u * 256;
+            if (k >= total) break;
+            const int i = (int)p.by_row.div(k);
+            ch[u] = k - i * chunks;
+            at[u] = first + i;
+            s[u] = load_stored<FMT>(p, p.rows ? __ldg(p.rows + at[u]) : p.row0 + at[u], ch[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (base + u * 256 >= total) break;
+            float v[8];
+            values_of<FMT>(s[u], ch[u], v);
+            T* dst = out + at[u] * p.out_ld + 8 * ch[u];
+            Eight<T> o;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o.e[k] = from_f32<T>(v[k]);
+            if (p.fast) {
+#pragma unroll
+                for (int w = 0; w < (int)sizeof(T) / 2; ++w) reinterpret_cast<uint4*>(dst)[w] = o.q[w];
             } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(part + 16 * (c / 4) + 8 * (c % 2)));
-                const uint32_t u[2] = {w.x, w.y};
-                const int shift = c % 4 < 2 ? 0 : 4;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[k] = d * (float)((int)(u[k / 4] >> (8 * (k % 4) + shift) & 0xfu) - 8);
+                for (int k = 0; k < 8; ++k) dst[k] = o.e[k];
             }
         }
-    }
-    T* dst = out + i * p.out_ld + 8 * c;
-    union { uint4 q[sizeof(T) / 2]; T e[8]; } o;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o.e[k] = from_f32<T>(v[k]);
-    if (p.fast) {
-#pragma unroll
-        for (int w = 0; w < (int)sizeof(T) / 2; ++w) reinterpret_cast<uint4*>(dst)[w] = o.q[w];
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = o.e[k];
     }
 }
 

@@ -12,8 +12,9 @@
 // exactly; the top 32 bits of the wrapped product are the angle that sincospif takes. What
 // is left is the frequency's own rounding, at most |position| * 2^-55 turns, and fp32's.
 //
-// Bound: memory (each value read and written once). cos and sin of a (token, pair) serve
-// every head, so a thread takes one chunk of a token's rotated dims for several heads.
+// Bound: memory (each value read and written once). A block takes a few tokens (or a slice
+// of one with very many heads): it computes their cos and sin once, into shared memory, for
+// all heads, then walks their chunks, four loads in flight per thread.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -58,6 +59,22 @@ struct alignas(V * sizeof(T)) Vec {
     T v[V];
 };
 
+// Quotients by a divisor d of values v with v * d < 2^32, as a multiplication by ceil(2^32 / d).
+struct SmallDiv {
+    uint32_t d, m;
+    __host__ void set(uint32_t divisor) {
+        d = divisor;
+        m = (uint32_t)(((1ull << 32) + divisor - 1) / divisor);      // 0 (2^32) for a divisor of 1
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t v) const { return m ? __umulhi(v, m) : v; }
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxHead = 32768;    // values of a head at most: (kRopeMaxHead + kRopeChunks) of
+                                       // its chunks times itself is below 2^32
+constexpr int kRopeChunks = 4096;      // chunks of a block at most
+constexpr int kRopeTurns = 2048;       // (token, pair) of a block at most
+
 struct RopeParams {
     RopeTable tab;
     const void* x;
@@ -67,108 +84,84 @@ struct RopeParams {
     long long pos0, pos_step;
     int n, heads;
     int rot, per_head;                 // chunks of a head: rotated, all of them
-    int groups;                        // heads / heads per thread, rounded up
+    int tokens;                        // tokens of a block; 1 where a token has several blocks
+    int slices;                        // blocks per token (tokens == 1)
+    SmallDiv by_head, by_token;        // chunks of a head, of a token
 };
 
 // A chunk is V values (two for V = 1 interleaved); a halves-layout chunk is V values of
 // the first half and their partners in the second. Chunks [0, rot) of a head are its
-// rotated dims, [rot, per_head) the dims copied beside them. Thread: one chunk of one
-// token for HPT heads, `groups` apart, so that a warp's accesses of one step are the
-// chunks of neighbouring heads.
-template <class T, int V, int HPT>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int C = V < 2 ? 2 : V;                      // values of an interleaved chunk
-    __shared__ uint64_t step[kRopeMaxDims / 2];
-    for (int i = threadIdx.x; i < p.tab.dims / 2; i += 256) step[i] = p.tab.step[i];
-    __syncthreads();
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int per_token = p.groups * p.per_head;
-    const long long tok = id / per_token;
-    if (tok >= p.n) return;
-    const int rest = (int)(id - tok * per_token), hg = rest / p.per_head, ch = rest - hg * p.per_head;
-    const T* x = static_cast<const T*>(p.x) + tok * p.x_ts;
-    T* out = static_cast<T*>(p.out) + tok * p.o_ts;
+// rotated dims, [rot, per_head) the dims copied beside them.
+template <class T, int V, bool HALVES>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int C = HALVES || V > 1 ? V : 2;            // values of a chunk (of each half)
+    constexpr int P = HALVES ? C : C / 2;                 // pairs of a chunk
+    constexpr int U = HALVES ? 2 : 4;                     // chunks in flight per thread: 64 bytes
+    extern __shared__ float2 turn[];                      // [token][pair]
     using W = Vec<T, V>;
-    if (ch >= p.rot) {                                    // a copied chunk
-        int d = (ch - p.rot) * V;
-        if (d >= p.tab.offset) d += p.tab.dims;
-#pragma unroll
-        for (int j = 0; j < HPT; ++j) {
-            const int h = hg + j * p.groups;
-            if (h < p.heads)
-                *reinterpret_cast<W*>(out + h * p.o_hs + d) = *reinterpret_cast<const W*>(x + h * p.x_hs + d);
-        }
-        return;
+    const int pairs = p.tab.dims / 2, tid = threadIdx.x;
+    const int tok0 = p.slices > 1 ? blockIdx.x / p.slices : blockIdx.x * p.tokens;
+    const int n_tok = min(p.tokens, p.n - tok0);
+    const int c0 = p.slices > 1 ? blockIdx.x % p.slices * kRopeChunks : 0;   // of the token's chunks
+    for (int i = tid; i < n_tok * pairs; i += kRopeThreads) {
+        const int t = i / pairs;
+        const long long pos = p.positions ? (long long)p.positions[tok0 + t] : p.pos0 + (tok0 + t) * p.pos_step;
+        const float2 cs = rope_turn(p.tab.step[i - t * pairs], pos, p.tab.m);
+        turn[i] = make_float2(cs.x, p.tab.transpose ? -cs.y : cs.y);
     }
-    const long long pos = p.positions ? (long long)p.positions[tok] : p.pos0 + tok * p.pos_step;
-    const float sign = p.tab.transpose ? -1.f : 1.f;
-    if (p.tab.half_layout) {
-        float2 cs[V];
+    __syncthreads();
+    const int h0 = c0 / p.per_head, first = c0 - h0 * p.per_head;
+    const int total = p.slices > 1 ? min(kRopeChunks, (int)p.by_token.d - c0) : n_tok * (int)p.by_token.d;
+#pragma unroll 1
+    for (int base = tid; base < total; base += U * kRopeThreads) {
+        const T* src[U];
+        T* dst[U];
+        const float2* cs[U];                              // NULL: a copied chunk
+        W a[U][HALVES ? 2 : C / V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            cs[i] = rope_turn(step[ch * V + i], pos, p.tab.m);
-            cs[i].y *= sign;
-        }
-        const int da = p.tab.offset + ch * V, db = da + p.tab.dims / 2;
-        W a[HPT], b[HPT];
-#pragma unroll
-        for (int j = 0; j < HPT; ++j) {
-            const int h = hg + j * p.groups;
-            if (h < p.heads) {
-                a[j] = *reinterpret_cast<const W*>(x + h * p.x_hs + da);
-                b[j] = *reinterpret_cast<const W*>(x + h * p.x_hs + db);
+        for (int u = 0; u < U; ++u) {
+            const int c = base + u * kRopeThreads;
+            if (c >= total) break;
+            const uint32_t t = p.slices > 1 ? 0 : p.by_token.div(c), in_tok = c - t * p.by_token.d + first;
+            const uint32_t hh = p.by_head.div(in_tok), h = hh + h0;
+            int ch = (int)(in_tok - hh * p.by_head.d), d;
+            if (ch < p.rot) {
+                cs[u] = turn + t * pairs + ch * P;
+                d = p.tab.offset + ch * C;
+            } else {
+                cs[u] = nullptr;
+                d = (ch - p.rot) * V;
+                if (d >= p.tab.offset) d += p.tab.dims;
+            }
+            src[u] = static_cast<const T*>(p.x) + (tok0 + (long long)t) * p.x_ts + h * p.x_hs + d;
+            dst[u] = static_cast<T*>(p.out) + (tok0 + (long long)t) * p.o_ts + h * p.o_hs + d;
+            a[u][0] = *reinterpret_cast<const W*>(src[u]);
+            if (cs[u]) {
+                if constexpr (HALVES) a[u][1] = *reinterpret_cast<const W*>(src[u] + pairs);
+                else if constexpr (C > V) a[u][1] = *reinterpret_cast<const W*>(src[u] + V);
             }
         }
 #pragma unroll
-        for (int j = 0; j < HPT; ++j) {
-            const int h = hg + j * p.groups;
-            if (h >= p.heads) continue;
-            W u, v;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float fa = to_f32(a[j].v[i]), fb = to_f32(b[j].v[i]);
-                u.v[i] = from_f32<T>(fa * cs[i].x - fb * cs[i].y);
-                v.v[i] = from_f32<T>(fa * cs[i].y + fb * cs[i].x);
+        for (int u = 0; u < U; ++u) {
+            if (base + u * kRopeThreads >= total) break;
+            if (!cs[u]) {
+                *reinterpret_cast<W*>(dst[u]) = a[u][0];
+                continue;
             }
-            *reinterpret_cast<W*>(out + h * p.o_hs + da) = u;
-            *reinterpret_cast<W*>(out + h * p.o_hs + db) = v;
-        }
-    } else {
-        float2 cs[C / 2];
+            W o[HALVES ? 2 : C / V];
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-            cs[i] = rope_turn(step[ch * (C / 2) + i], pos, p.tab.m);
-            cs[i].y *= sign;
-        }
-        const int d = p.tab.offset + ch * C;
-        W a[HPT][C / V];
-#pragma unroll
-        for (int j = 0; j < HPT; ++j) {
-            const int h = hg + j * p.groups;
-            if (h < p.heads)
-#pragma unroll
-                for (int w = 0; w < C / V; ++w)
-                    a[j][w] = *reinterpret_cast<const W*>(x + h * p.x_hs + d + w * V);
-        }
-#pragma unroll
-        for (int j = 0; j < HPT; ++j) {
-            const int h = hg + j * p.groups;
-            if (h >= p.heads) continue;
-            T r[C];
-#pragma unroll
-            for (int i = 0; i < C / 2; ++i) {
-                const float fa = to_f32(a[j][2 * i / V].v[2 * i % V]);
-                const float fb = to_f32(a[j][(2 * i + 1) / V].v[(2 * i + 1) % V]);
-                r[2 * i] = from_f32<T>(fa * cs[i].x - fb * cs[i].y);
-                r[2 * i + 1] = from_f32<T>(fa * cs[i].y + fb * cs[i].x);
+            for (int i = 0; i < P; ++i) {
+                const float2 r = cs[u][i];
+                // the pair's places in the loaded vectors
+                const int va = HALVES ? 0 : 2 * i / V, ia = HALVES ? i : 2 * i % V;
+                const int vb = HALVES ? 1 : (2 * i + 1) / V, ib = HALVES ? i : (2 * i + 1) % V;
+                const float fa = to_f32(a[u][va].v[ia]), fb = to_f32(a[u][vb].v[ib]);
+                o[va].v[ia] = from_f32<T>(fa * r.x - fb * r.y);
+                o[vb].v[ib] = from_f32<T>(fa * r.y + fb * r.x);
             }
-#pragma unroll
-            for (int w = 0; w < C / V; ++w) {
-                W o;
-#pragma unroll
-                for (int i = 0; i < V; ++i) o.v[i] = r[w * V + i];
-                *reinterpret_cast<W*>(out + h * p.o_hs + d + w * V) = o;
-            }
+            *reinterpret_cast<W*>(dst[u]) = o[0];
+            if constexpr (HALVES) *reinterpret_cast<W*>(dst[u] + pairs) = o[1];
+            else if constexpr (C > V) *reinterpret_cast<W*>(dst[u] + V) = o[1];
         }
     }
 }

@@ -8,6 +8,7 @@ missing the first call raises ``Ds4spError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Dict, List, Optional, Tuple
@@ -140,8 +141,10 @@ def _kv_dtype(t) -> torch.dtype:
 
 
 def _stream(stream=None) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    # (the handle itself: building torch's Stream object takes longer than the library call)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 # ------------------------------------------------------------------ handle
@@ -342,10 +345,15 @@ def make_rope(dims: int, offset: int = 0, layout: int = 0, base: float = 10000.0
                              mscale)
 
 
+def _device() -> int:
+    """The current CUDA device, which host tensors (device -1) are not on."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
 def _rows(t: torch.Tensor, name: str, dims: int) -> int:
     """The dtype code of a strided device tensor of `dims` dimensions whose last one is
     contiguous. It belongs to the current device, whose stream the call uses."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != _device():
         raise Ds4spError(ERR_INVALID_ARG, name, "tensor must be on the current CUDA device")
     if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise Ds4spError(ERR_INVALID_ARG, name, f"expected {dims} dimensions, the last one contiguous")
@@ -358,7 +366,7 @@ def _rows(t: torch.Tensor, name: str, dims: int) -> int:
 def _int_rows(t: Optional[torch.Tensor], name: str, n: int) -> Optional[int]:
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != torch.cuda.current_device() or t.dtype != torch.int32 \
+    if t.get_device() != _device() or t.dtype != torch.int32 \
             or not t.is_contiguous() or t.numel() != n:
         raise Ds4spError(ERR_INVALID_ARG, name, f"expected a contiguous int32 tensor of {n} on the current device")
     return t.data_ptr()
@@ -372,7 +380,7 @@ def ds4sp_rope(x, rope: ds4sp_rope_config, out=None, positions=None, pos0: int =
     transpose: the transposed rotation, the gradient with respect to x."""
     code = _rows(x, "x", 3)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     elif _rows(out, "out", 3) != code or out.shape != x.shape:
         raise Ds4spError(ERR_INVALID_ARG, "out", f"expected {x.dtype} {tuple(x.shape)}")
     n, heads, head = x.shape
@@ -387,14 +395,20 @@ def ds4sp_cache_bytes(kv_format: int, dims: int, rows: int) -> int:
     return int(load_library().ds4sp_cache_bytes(kv_format, dims, rows))
 
 
+@functools.lru_cache(maxsize=64)
+def _cache_unit(kv_format: int, dims: int) -> Tuple[int, int]:
+    """The rows a cache grows by, and their bytes."""
+    unit = SCALE_BLOCK if kv_format == 5 else 1
+    return unit, ds4sp_cache_bytes(kv_format, dims, unit)
+
+
 def _cache(cache: torch.Tensor, kv_format: int, dims: int) -> int:
     """Rows that a cache tensor (uint8, or float16 rows) holds in a format."""
-    if not cache.is_cuda or cache.device.index != torch.cuda.current_device() or not cache.is_contiguous():
+    if cache.get_device() != _device() or not cache.is_contiguous():
         raise Ds4spError(ERR_INVALID_ARG, "cache", "expected a contiguous tensor on the current CUDA device")
     if cache.dtype != torch.uint8 and not (kv_format == 0 and cache.dtype == torch.float16):
         raise Ds4spError(ERR_INVALID_ARG, "cache", f"dtype {cache.dtype}, expected uint8 (or float16 rows)")
-    unit = SCALE_BLOCK if kv_format == 5 else 1
-    size = ds4sp_cache_bytes(kv_format, dims, unit)
+    unit, size = _cache_unit(kv_format, dims)
     if size == 0:
         raise Ds4spError(ERR_INVALID_ARG, "cache", f"kv_format {kv_format} with rows of {dims} values")
     return cache.numel() * cache.element_size() // size * unit
