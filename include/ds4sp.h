@@ -385,7 +385,7 @@ typedef struct {
 /* Turn the rotary part of x [n_tokens, heads, head_dim] into out (the attention takes its
  * queries and rows after rotation). Token and head strides are in values; the values of a
  * head are contiguous, at the alignment of their type (16-byte aligned rows are faster).
- * The head's other values are copied; head_dim is at most 32,768. out may be x with the same strides (in place);
+ * The head's other values are copied; head_dim is at most 2^20. out may be x with the same strides (in place);
  * otherwise the two must not share elements, and out's heads must not overlap one another.
  *   positions  [n_tokens] int32 (device), or NULL: row i is at pos0 + i * pos_step (raw
  *              rows: the token and 1; compressed row j: 4 * j and 4)

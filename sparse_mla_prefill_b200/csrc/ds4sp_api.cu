@@ -963,7 +963,7 @@ ds4sp_status make_rope_table(const ds4sp_rope_config* cfg, RopeTable* tab) {
 }
 
 template <class T, int V>
-void launch_rope_v(RopeParams& p, unsigned grid, cudaStream_t s) {
+void launch_rope_v(RopeParams& p, dim3 grid, cudaStream_t s) {
     const size_t smem = (size_t)p.tokens * (p.tab.dims / 2) * sizeof(float2);
     if (p.tab.half_layout)
         rope_kernel<T, V, true><<<grid, kRopeThreads, smem, s>>>(p);
@@ -972,34 +972,25 @@ void launch_rope_v(RopeParams& p, unsigned grid, cudaStream_t s) {
 }
 
 template <class T>
-void launch_rope_t(RopeParams& p, int v, unsigned grid, cudaStream_t s) {
+void launch_rope_t(RopeParams& p, int v, dim3 grid, cudaStream_t s) {
     if (v > 2) launch_rope_v<T, 16 / sizeof(T)>(p, grid, s);
     else if (v == 2) launch_rope_v<T, 2>(p, grid, s);
     else launch_rope_v<T, 1>(p, grid, s);
 }
 
-// Tokens of a block: about 2,048 chunks' worth, as long as that leaves two blocks an SM (a
-// small call spreads its tokens, where latency counts); a token of more than kRopeChunks
-// chunks takes several blocks.
+// Tokens of a block: those whose rows its threads load at once, as long as that leaves two
+// blocks an SM (a small call spreads its tokens, where latency counts).
 ds4sp_status launch_rope(RopeParams& p, ds4sp_dtype t, int v, cudaStream_t s) {
-    const long long per_token = (long long)p.heads * p.per_head;
-    if (per_token > 0x7fffffffLL / 2)
-        return fail(DS4SP_ERR_INVALID_ARG, "%d heads of %d chunks is too many", p.heads, p.per_head);
-    p.slices = 1;
-    p.tokens = 1;
-    if (per_token > kRopeChunks) {
-        p.slices = (int)((per_token + kRopeChunks - 1) / kRopeChunks);
-    } else {
-        const long long most = std::min<long long>(2048 / per_token, kRopeTurns / (p.tab.dims / 2));
-        p.tokens = (int)std::max<long long>(1, std::min<long long>(most, p.n / 296));
-    }
-    p.by_head.set((uint32_t)p.per_head);
-    p.by_token.set((uint32_t)per_token);
-    const long long blocks = p.slices > 1 ? (long long)p.n * p.slices : (p.n + p.tokens - 1) / p.tokens;
-    if (blocks > 0x7fffffffLL) return fail(DS4SP_ERR_INVALID_ARG, "%d tokens of %d heads is too many", p.n, p.heads);
-    if (t == DS4SP_F32) launch_rope_t<float>(p, v, (unsigned)blocks, s);
-    else if (t == DS4SP_BF16) launch_rope_t<__nv_bfloat16>(p, v, (unsigned)blocks, s);
-    else launch_rope_t<__half>(p, v, (unsigned)blocks, s);
+    const int width = std::min(p.per_head, kRopeThreads);
+    p.groups = kRopeThreads / width;
+    const long long most = std::min<long long>((long long)rope_rows(p.tab.half_layout) * p.groups / p.heads, kRopeTurns / (p.tab.dims / 2));
+    p.tokens = (int)std::max<long long>(1, std::min<long long>(most, p.n / 296));
+    p.by_width.set((uint32_t)width);
+    p.by_heads.set((uint32_t)p.heads);
+    const dim3 grid((unsigned)((p.n + p.tokens - 1) / p.tokens), (unsigned)((p.per_head + width - 1) / width));
+    if (t == DS4SP_F32) launch_rope_t<float>(p, v, grid, s);
+    else if (t == DS4SP_BF16) launch_rope_t<__nv_bfloat16>(p, v, grid, s);
+    else launch_rope_t<__half>(p, v, grid, s);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DS4SP_OK : cuda_fail(e, "rope launch");
 }
@@ -1508,7 +1499,7 @@ ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype
     DS4SP_TRY(rope_table(cfg, transpose, &p.tab));
     const int es = dtype_bytes(dtype);
     if (es == 0) return fail(DS4SP_ERR_INVALID_ARG, "dtype %d", (int)dtype);
-    if (n_tokens < 0 || heads < 1 || head_dim < 1 || head_dim > kRopeMaxHead)
+    if (n_tokens < 0 || heads < 1 || head_dim < 1 || head_dim > (1 << 20))
         return fail(DS4SP_ERR_INVALID_ARG, "n_tokens %d, heads %d, head_dim %d", n_tokens, heads, head_dim);
     if ((long long)cfg->offset + cfg->dims > head_dim)
         return fail(DS4SP_ERR_INVALID_ARG, "rotary dims [%d, %d) of a head of %d", cfg->offset,

@@ -79,10 +79,16 @@ __device__ __forceinline__ bool turned(const CacheRows& p, const RopeTable& tab,
     return p.rotate && 8 * c >= tab.offset && 8 * c < tab.offset + tab.dims;
 }
 
-// A rotated chunk c of row i, loaded as `a`, in fp32 (p.fast).
+struct Floats {
+    float v[8];
+};
+
+// A rotated chunk c of row i, loaded as `a`, in fp32 (p.fast). Out of line: a thread's steps are
+// unrolled, and one or two of them are rotated.
 template <class T>
-__device__ __forceinline__ void turn_eight(const CacheRows& p, const RopeTable& tab, const uint64_t* step, int i,
-                                           int c, const Eight<T>& a, float (&v)[8]) {
+__device__ __noinline__ Floats turn_eight(const CacheRows& p, const RopeTable& tab, const uint64_t* step, int i,
+                                          int c, Eight<T> a) {
+    float v[8];
     const long long pos = position_of(p, i);
     const int r0 = 8 * c - tab.offset, half = tab.dims / 2;
     if (tab.half_layout) {
@@ -103,6 +109,10 @@ __device__ __forceinline__ void turn_eight(const CacheRows& p, const RopeTable& 
             v[2 * k + 1] = a0 * cs.y + b0 * cs.x;
         }
     }
+    Floats out;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out.v[k] = v[k];
+    return out;
 }
 
 // Eight values of row i (of the n written) at dims 8c .. 8c+7, rotated, in fp32.
@@ -113,12 +123,10 @@ __device__ __forceinline__ void load_chunk(const CacheRows& p, const RopeTable& 
     const int d0 = 8 * c;
     if (p.fast) {
         const Eight<T> a = load_eight(row + d0);
-        if (turned(p, tab, c)) {
-            turn_eight<T>(p, tab, step, i, c, a, v);
-        } else {
+        const bool t = turned(p, tab, c);
+        const Floats f = t ? turn_eight<T>(p, tab, step, i, c, a) : Floats{};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = to_f32(a.e[k]);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = t ? f.v[k] : to_f32(a.e[k]);
         return;
     }
     const long long pos = p.rotate ? position_of(p, i) : 0;
@@ -171,7 +179,7 @@ __device__ __forceinline__ uint2 q4_codes(const float (&v)[8], float d) {
 // Rows are stored at out + row * row_bytes. FMT: kFmtF16, kFmtQ8, kFmtQ4 or kFmtQ8Q4.
 template <class T, int FMT>
 __global__ void __launch_bounds__(256)
-cache_write_kernel(const CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ out,
+cache_write_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ out,
                    int row_bytes) {
     __shared__ uint64_t step[kRopeMaxDims / 2];
     load_steps(tab, p.rotate, step);
@@ -266,6 +274,34 @@ __device__ __forceinline__ float top_of(const float (&u)[8], float top) {
     }
     return top;
 }
+template <class T>
+__device__ __forceinline__ float top_of(const Eight<T>& a, float top) {
+    float u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = to_f32(a.e[k]);
+    return top_of(u, top);
+}
+
+// Magnitudes as integers: without its sign a float orders as its bits do. The larger of `bits`
+// (one 32-bit value, or two 16-bit ones) and a chunk's, infinities and NaNs included.
+template <class T>
+__device__ __forceinline__ uint32_t top_bits(const Eight<T>& a, uint32_t bits) {
+#pragma unroll
+    for (int w = 0; w < (int)sizeof(T) / 2; ++w) {
+        const uint32_t u[4] = {a.q[w].x, a.q[w].y, a.q[w].z, a.q[w].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            bits = sizeof(T) == 4 ? max(bits, u[k] & 0x7fffffffu) : __vmaxu2(bits, u[k] & 0x7fff7fffu);
+    }
+    return bits;
+}
+__device__ __forceinline__ float top_value(uint32_t bits, float) { return __uint_as_float(bits); }
+__device__ __forceinline__ float top_value(uint32_t bits, __half) {
+    return __half2float(__ushort_as_half((unsigned short)max(bits & 0xffffu, bits >> 16)));
+}
+__device__ __forceinline__ float top_value(uint32_t bits, __nv_bfloat16) {
+    return __uint_as_float(max(bits & 0xffffu, bits >> 16) << 16);
+}
 
 // One CTA per block of 64 rows that the write touches; eight lanes a row, each taking every
 // eighth chunk of eight values. HELD (up to 576 dims, aligned): the values as they were loaded
@@ -275,7 +311,7 @@ __device__ __forceinline__ float top_of(const float (&u)[8], float top) {
 // twice.
 template <class T, bool HELD>
 __global__ void __launch_bounds__(kE4M3Threads, sizeof(T) == 2 ? 2 : 1)
-cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ cache) {
+cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ cache) {
     __shared__ uint64_t step[kRopeMaxDims / 2];
     __shared__ float warp_top[kE4M3Threads / 32];
     const int tid = threadIdx.x, r = tid / 8, l = tid % 8;
@@ -300,18 +336,26 @@ cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab
     float top = 0.f;
     if (in) {
         if constexpr (HELD) {
+            uint32_t bits = 0u;
 #pragma unroll
             for (int s = 0; s < kE4M3Held; ++s) {
                 const int c = 8 * s + l;
                 if (c >= chunks) continue;
-                float u[8];
                 if (turned(p, tab, c)) {
-                    turn_eight<T>(p, tab, step, i, c, v[s], u);
+                    top = top_of(turn_eight<T>(p, tab, step, i, c, v[s]).v, top);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) u[k] = to_f32(v[s].e[k]);
+                    bits = top_bits<T>(v[s], bits);
                 }
-                top = top_of(u, top);
+            }
+            const float t = top_value(bits, T{});
+            if (t <= 3.402823466e38f) {
+                top = fmaxf(top, t);
+            } else {                                      // an infinity or a NaN: the finite ones
+#pragma unroll
+                for (int s = 0; s < kE4M3Held; ++s) {
+                    const int c = 8 * s + l;
+                    if (c < chunks && !turned(p, tab, c)) top = top_of<T>(v[s], top);
+                }
             }
         } else {
             for (int c = l; c < chunks; c += 8) {
@@ -360,13 +404,13 @@ cache_write_e4m3_kernel(const CacheRows p, const __grid_constant__ RopeTable tab
         for (int s = 0; s < kE4M3Held; ++s) {
             const int c = 8 * s + l;
             if (c >= chunks) continue;
-            float u[8];
             if (turned(p, tab, c)) {
-                turn_eight<T>(p, tab, step, i, c, v[s], u);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) u[k] = to_f32(v[s].e[k]);
+                put(c, turn_eight<T>(p, tab, step, i, c, v[s]).v);
+                continue;
             }
+            float u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = to_f32(v[s].e[k]);
             put(c, u);
         }
     } else {

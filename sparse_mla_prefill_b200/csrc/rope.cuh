@@ -12,9 +12,9 @@
 // exactly; the top 32 bits of the wrapped product are the angle that sincospif takes. What
 // is left is the frequency's own rounding, at most |position| * 2^-55 turns, and fp32's.
 //
-// Bound: memory (each value read and written once). A block takes a few tokens (or a slice
-// of one with very many heads): it computes their cos and sin once, into shared memory, for
-// all heads, then walks their chunks, four loads in flight per thread.
+// Bound: memory (each value read and written once). A thread keeps one chunk of the head and
+// walks rows (token, head), four loads in flight; the block computes its tokens' cos and sin
+// once, into shared memory, for all heads, while its first loads are on their way.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,6 +53,25 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(v);
 }
 
+// Two neighbouring values as fp32, and back, rounded once: one 32-bit word for 16-bit types.
+__device__ __forceinline__ float2 pair_f32(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 pair_f32(const __half* v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(v));
+}
+__device__ __forceinline__ float2 pair_f32(const __nv_bfloat16* v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(v));
+}
+__device__ __forceinline__ void put_pair(float* v, float a, float b) {
+    v[0] = a;
+    v[1] = b;
+}
+__device__ __forceinline__ void put_pair(__half* v, float a, float b) {
+    *reinterpret_cast<__half2*>(v) = __floats2half2_rn(a, b);
+}
+__device__ __forceinline__ void put_pair(__nv_bfloat16* v, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162*>(v) = __floats2bfloat162_rn(a, b);
+}
+
 // V values moved as one access of V * sizeof(T) bytes.
 template <class T, int V>
 struct alignas(V * sizeof(T)) Vec {
@@ -70,10 +89,8 @@ struct SmallDiv {
 };
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxHead = 32768;    // values of a head at most: (kRopeMaxHead + kRopeChunks) of
-                                       // its chunks times itself is below 2^32
-constexpr int kRopeChunks = 4096;      // chunks of a block at most
 constexpr int kRopeTurns = 2048;       // (token, pair) of a block at most
+constexpr int rope_rows(bool halves) { return halves ? 2 : 4; }    // rows in flight per thread
 
 struct RopeParams {
     RopeTable tab;
@@ -84,25 +101,45 @@ struct RopeParams {
     long long pos0, pos_step;
     int n, heads;
     int rot, per_head;                 // chunks of a head: rotated, all of them
-    int tokens;                        // tokens of a block; 1 where a token has several blocks
-    int slices;                        // blocks per token (tokens == 1)
-    SmallDiv by_head, by_token;        // chunks of a head, of a token
+    int tokens;                        // tokens of a block (heads * tokens below 2^16 where above 1)
+    int groups;                        // rows a block walks side by side
+    SmallDiv by_width, by_heads;       // threads of a row, heads of a token
 };
 
 // A chunk is V values (two for V = 1 interleaved); a halves-layout chunk is V values of
 // the first half and their partners in the second. Chunks [0, rot) of a head are its
-// rotated dims, [rot, per_head) the dims copied beside them.
+// rotated dims, [rot, per_head) the dims copied beside them. blockIdx.y counts chunks by the
+// width of a row where a head has more of them than the block threads.
 template <class T, int V, bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int C = HALVES || V > 1 ? V : 2;            // values of a chunk (of each half)
     constexpr int P = HALVES ? C : C / 2;                 // pairs of a chunk
-    constexpr int U = HALVES ? 2 : 4;                     // chunks in flight per thread: 64 bytes
+    constexpr int U = rope_rows(HALVES);                  // 64 bytes of wide accesses
+    constexpr int L = HALVES || C > V ? 2 : 1;            // accesses of a chunk
     extern __shared__ float2 turn[];                      // [token][pair]
     using W = Vec<T, V>;
-    const int pairs = p.tab.dims / 2, tid = threadIdx.x;
-    const int tok0 = p.slices > 1 ? blockIdx.x / p.slices : blockIdx.x * p.tokens;
-    const int n_tok = min(p.tokens, p.n - tok0);
-    const int c0 = p.slices > 1 ? blockIdx.x % p.slices * kRopeChunks : 0;   // of the token's chunks
+    const int pairs = p.tab.dims / 2, tid = threadIdx.x, apart = HALVES ? pairs : V;
+    const int tok0 = blockIdx.x * p.tokens, n_tok = min(p.tokens, p.n - tok0);
+    const int group = (int)p.by_width.div(tid), ch = tid - group * (int)p.by_width.d + blockIdx.y * (int)p.by_width.d;
+    const bool rot = ch < p.rot;
+    const int rows = group < p.groups && ch < p.per_head ? n_tok * p.heads : 0;
+    int d = rot ? p.tab.offset + ch * C : (ch - p.rot) * V;
+    if (!rot && d >= p.tab.offset) d += p.tab.dims;
+    const T* x = static_cast<const T*>(p.x) + tok0 * p.x_ts + d;
+    T* out = static_cast<T*>(p.out) + tok0 * p.o_ts + d;
+    W a[U][L];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = r0 + u * p.groups;
+            if (row >= rows) break;
+            const int t = p.tokens > 1 ? (int)p.by_heads.div(row) : 0, h = row - t * p.heads;
+            const T* src = x + t * p.x_ts + h * p.x_hs;
+            a[u][0] = *reinterpret_cast<const W*>(src);
+            if (L > 1 && rot) a[u][L - 1] = *reinterpret_cast<const W*>(src + apart);
+        }
+    };
+    load(group);
     for (int i = tid; i < n_tok * pairs; i += kRopeThreads) {
         const int t = i / pairs;
         const long long pos = p.positions ? (long long)p.positions[tok0 + t] : p.pos0 + (tok0 + t) * p.pos_step;
@@ -110,58 +147,44 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
         turn[i] = make_float2(cs.x, p.tab.transpose ? -cs.y : cs.y);
     }
     __syncthreads();
-    const int h0 = c0 / p.per_head, first = c0 - h0 * p.per_head;
-    const int total = p.slices > 1 ? min(kRopeChunks, (int)p.by_token.d - c0) : n_tok * (int)p.by_token.d;
+    float2 cs[P];                                         // of the token held
+    int held = -1;
 #pragma unroll 1
-    for (int base = tid; base < total; base += U * kRopeThreads) {
-        const T* src[U];
-        T* dst[U];
-        const float2* cs[U];                              // NULL: a copied chunk
-        W a[U][HALVES ? 2 : C / V];
+    for (int r0 = group; r0 < rows; r0 += U * p.groups) {
+        if (r0 != group) load(r0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = base + u * kRopeThreads;
-            if (c >= total) break;
-            const uint32_t t = p.slices > 1 ? 0 : p.by_token.div(c), in_tok = c - t * p.by_token.d + first;
-            const uint32_t hh = p.by_head.div(in_tok), h = hh + h0;
-            int ch = (int)(in_tok - hh * p.by_head.d), d;
-            if (ch < p.rot) {
-                cs[u] = turn + t * pairs + ch * P;
-                d = p.tab.offset + ch * C;
-            } else {
-                cs[u] = nullptr;
-                d = (ch - p.rot) * V;
-                if (d >= p.tab.offset) d += p.tab.dims;
-            }
-            src[u] = static_cast<const T*>(p.x) + (tok0 + (long long)t) * p.x_ts + h * p.x_hs + d;
-            dst[u] = static_cast<T*>(p.out) + (tok0 + (long long)t) * p.o_ts + h * p.o_hs + d;
-            a[u][0] = *reinterpret_cast<const W*>(src[u]);
-            if (cs[u]) {
-                if constexpr (HALVES) a[u][1] = *reinterpret_cast<const W*>(src[u] + pairs);
-                else if constexpr (C > V) a[u][1] = *reinterpret_cast<const W*>(src[u] + V);
-            }
-        }
+            const int row = r0 + u * p.groups;
+            if (row >= rows) break;
+            const int t = p.tokens > 1 ? (int)p.by_heads.div(row) : 0, h = row - t * p.heads;
+            if (rot) {
+                if (t != held) {
+                    held = t;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (base + u * kRopeThreads >= total) break;
-            if (!cs[u]) {
-                *reinterpret_cast<W*>(dst[u]) = a[u][0];
-                continue;
-            }
-            W o[HALVES ? 2 : C / V];
+                    for (int i = 0; i < P; ++i) cs[i] = turn[t * pairs + ch * P + i];
+                }
+                if constexpr (HALVES && V > 1) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 r = cs[u][i];
-                // the pair's places in the loaded vectors
-                const int va = HALVES ? 0 : 2 * i / V, ia = HALVES ? i : 2 * i % V;
-                const int vb = HALVES ? 1 : (2 * i + 1) / V, ib = HALVES ? i : (2 * i + 1) % V;
-                const float fa = to_f32(a[u][va].v[ia]), fb = to_f32(a[u][vb].v[ib]);
-                o[va].v[ia] = from_f32<T>(fa * r.x - fb * r.y);
-                o[vb].v[ib] = from_f32<T>(fa * r.y + fb * r.x);
+                    for (int i = 0; i < P; i += 2) {
+                        const float2 fa = pair_f32(&a[u][0].v[i]), fb = pair_f32(&a[u][1].v[i]);
+                        put_pair(&a[u][0].v[i], fa.x * cs[i].x - fb.x * cs[i].y, fa.y * cs[i + 1].x - fb.y * cs[i + 1].y);
+                        put_pair(&a[u][1].v[i], fa.x * cs[i].y + fb.x * cs[i].x, fa.y * cs[i + 1].y + fb.y * cs[i + 1].x);
+                    }
+                } else if constexpr (V > 1) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float2 f = pair_f32(&a[u][0].v[2 * i]);
+                        put_pair(&a[u][0].v[2 * i], f.x * cs[i].x - f.y * cs[i].y, f.x * cs[i].y + f.y * cs[i].x);
+                    }
+                } else {
+                    const float fa = to_f32(a[u][0].v[0]), fb = to_f32(a[u][1].v[0]);
+                    a[u][0].v[0] = from_f32<T>(fa * cs[0].x - fb * cs[0].y);
+                    a[u][1].v[0] = from_f32<T>(fa * cs[0].y + fb * cs[0].x);
+                }
             }
-            *reinterpret_cast<W*>(dst[u]) = o[0];
-            if constexpr (HALVES) *reinterpret_cast<W*>(dst[u] + pairs) = o[1];
-            else if constexpr (C > V) *reinterpret_cast<W*>(dst[u] + V) = o[1];
+            T* dst = out + t * p.o_ts + h * p.o_hs;
+            *reinterpret_cast<W*>(dst) = a[u][0];
+            if (L > 1 && rot) *reinterpret_cast<W*>(dst + apart) = a[u][L - 1];
         }
     }
 }
