@@ -11,14 +11,15 @@
 //   S   = codes . [a0 a1 a2]^T               M = 128 rows, N = 3 x 16, K = 576
 //   w   = 2^(s_r 2^e_h scale log2(e) S + log2 s_r - ref_h)      the row's scale joins its
 //                                            weight, since w * code = p * value
-//   w   = b0 + b1 / 16 + ... + b_{NT-1} / 16^(NT-1)
+//   w   = b0 + b1 / 16 + b2 / 2^9 (+ b3 / 2^13 + b4 / 2^18)
 //   O^T = codes^T . [b0 .. b_{NT-1}]         M = 128 value dims x 4, N = NT x 16, K = rows
 //   out = O / sum(w / s_r)
 //
-// w is split as hi + lo, hi its fp16 rounding: three terms hold hi (NT = 3, pv_mode 0: fp16
-// probabilities), two more lo to 2^-20 of w (NT = 5, pv_mode 1: the result is right to fp32
-// sums). Each rounding to e4m3 is of what the terms before it left, so nothing is lost but the
-// last one's remainder, and products of e4m3 values are exact in the fp32 accumulator.
+// NT = 3 terms hold the weight's fp16 rounding (pv_mode 0: fp16 probabilities), five the weight
+// to 2^-20, and to 2^-28 of a weight of 1 where it is small (pv_mode 1: the result is right to
+// fp32 sums; four terms would leave small weights 2^-23, 3e-6 of the result). Each rounding to
+// e4m3 is of what the terms before it left, so nothing is lost but the last one's remainder.
+// Products of e4m3 values are exact in the fp32 accumulator.
 //
 // What bounds it: each unit's rows pass through the tensor cores twice, from shared memory.
 // An M = 128, K = 32 instruction takes about 50 cycles whatever N up to 80 (measured: its
@@ -32,9 +33,10 @@
 // Roles: warps 0-7 softmax, 8-11 the queries' terms and the output, 12-15 gather (16-byte
 // cp.async), warp 16 issues S and warp 17 O^T: an MMA of this size is short
 // against a wait's latency, and with two issuers each one's waits run under the other's MMAs.
-// The reference ref_h is set 2^3 above the first unit's maximum, and raised (O and the sums
-// rescaled) only when a unit exceeds it by 2^8, e4m3 holding weights up to 448: for logits of
-// wide spread one unit in seven, against one in three with the maximum itself.
+// The reference ref_h is set above the first unit's maximum (by 2^5 with five terms), and
+// raised, O and the sums rescaled, only when a unit exceeds it by 2^8, e4m3 holding weights up
+// to 448: for logits of wide spread one unit in ten, against one in three with the maximum
+// itself.
 // Every wait is bounded; a wait that gives up sets the launch's abort word and every role
 // drains.
 #pragma once
@@ -62,8 +64,8 @@ constexpr int EWARP0 = SWARPS, PWARP0 = EWARP0 + EWARPS, SMMA = PWARP0 + PWARPS,
 constexpr int THREADS = (OMMA + 1) * 32;
 constexpr int SOFTMAX_BAR = 1;                  // and 2: one per group
 constexpr int OUT_BAR = 3;
-constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference, which
-constexpr float START = 3.f;                    // is set so many above a unit's maximum
+constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference, which is
+constexpr float start_of(int nt) { return nt == 5 ? 5.f : 3.f; }   // set so many above a unit's maximum
 
 constexpr int OFF_SLAB = 0;
 constexpr int OFF_ROPE = OFF_SLAB + SLOTS * SLAB;
@@ -92,12 +94,16 @@ static_assert(SMEM_BYTES <= attn::SMEM_LIMIT, "shared memory budget");
 constexpr int TM_S = 0, TM_O = 2 * QROWS, TM_SUM = 480;
 template <int NT> constexpr int o_cols() { return NT * H; }
 // The columns' order: term t of heads 8g .. 8g+7 (softmax group g) starts at o_col(g, t), so
-// that a thread's terms are 16-byte chunks: pairs of terms, and the last one beside the other
-// group's.
+// that a thread's terms are 16-byte chunks: pairs of terms, and an odd last one beside the
+// other group's.
 template <int NT>
 __host__ __device__ constexpr int o_col(int g, int t) {
-    return t + 1 < NT ? (g * (NT - 1) / 2 + t / 2) * H + t % 2 * HG : (NT - 1) * H + g * HG;
+    return t < NT / 2 * 2 ? (g * (NT / 2) + t / 2) * H + t % 2 * HG : NT / 2 * 2 * H + g * HG;
 }
+// Term t of a weight counts 1 / (the product of its steps): what a term leaves, times the step.
+// A term of up to 448 leaves up to 16, so 16 always fits; 32 does where the term is at most
+// 256, as the second is (it is 16 times what the first left of at most 256).
+__host__ __device__ constexpr float term_step(int t) { return t % 2 ? 32.f : 16.f; }
 static_assert(TM_O + TILES * o_cols<5>() <= TM_SUM && TM_SUM + 2 * H <= 512, "TMEM columns");
 
 // Shared-memory descriptors (start address added): K-major rows of 128 bytes (8-row groups
@@ -110,7 +116,6 @@ __host__ __device__ constexpr uint64_t desc_bits(uint32_t lbo, uint32_t sbo, uin
 }
 constexpr uint64_t DESC_128 = desc_bits(16, 1024, 2), DESC_64 = desc_bits(16, 512, 4),
                    DESC_P = desc_bits(128, M * H, 0);
-__device__ __forceinline__ uint64_t desc_at(uint64_t bits, uint32_t addr) { return bits | (addr >> 4); }
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D; tr: both operands MN-major.
 __host__ __device__ constexpr uint32_t idesc(int n, bool tr) {
@@ -118,22 +123,28 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool tr) {
 }
 
 // n (1 .. 4) MMAs in a row whose operands' addresses step by A_STEP and B_STEP bytes, executed
-// by a whole warp and issued by its elected lane (the same one every time). acc0: whether the
-// first accumulates; the others do.
-template <int A_STEP, int B_STEP>
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc0, int n) {
+// by a whole warp and issued by its elected lane (the same one every time). A_BITS, B_BITS: the
+// descriptors' layouts (desc_bits); a, b: the operands' addresses. acc0: whether the first
+// accumulates; the others do.
+template <uint64_t A_BITS, uint64_t B_BITS, int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t id, uint32_t acc0, int n) {
     asm volatile(
-        "{\n\t.reg .pred p, e, q, t;\n\t.reg .b64 a, b;\n\t"
+        "{\n\t.reg .pred p, e, q, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
         "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-        "add.s64 a, %1, %6;\n\tadd.s64 b, %2, %7;\n\tsetp.gt.and.s32 q, %5, 1, e;\n\t"
+        "mov.b32 x, %1;\n\tmov.b32 y, %2;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %7};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t"
+        "add.s32 x, x, %8;\n\tadd.s32 y, y, %9;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %7};\n\t"
+        "setp.gt.and.s32 q, %5, 1, e;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
-        "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\tsetp.gt.and.s32 q, %5, 2, e;\n\t"
+        "add.s32 x, x, %8;\n\tadd.s32 y, y, %9;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %7};\n\t"
+        "setp.gt.and.s32 q, %5, 2, e;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
-        "add.s64 a, a, %6;\n\tadd.s64 b, b, %7;\n\tsetp.gt.and.s32 q, %5, 3, e;\n\t"
+        "add.s32 x, x, %8;\n\tadd.s32 y, y, %9;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %7};\n\t"
+        "setp.gt.and.s32 q, %5, 3, e;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(id), "r"(acc0), "r"(n), "n"(A_STEP >> 4), "n"(B_STEP >> 4)
+        "r"((uint32_t)A_BITS | a >> 4), "r"((uint32_t)B_BITS | b >> 4), "r"(id), "r"(acc0), "r"(n),
+        "n"((uint32_t)(A_BITS >> 32)), "n"((uint32_t)(B_BITS >> 32)), "n"(A_STEP >> 4), "n"(B_STEP >> 4)
         : "memory");
 }
 // An arrival when all MMAs issued so far complete.
@@ -234,13 +245,43 @@ struct Cursor {
     __device__ __forceinline__ int rows() const { return min(M, it.rows - M * u); }
 };
 
-// fp16 -> e4m3 codes of a pair, and what they leave, times 16 (exact: the difference of an
+// fp16 -> e4m3 codes of a pair, and what they leave, times `step` (exact: the difference of an
 // fp16 value and its rounding to fewer bits is an fp16 value).
 __device__ __forceinline__ uint32_t e4m3x2_of(__half2 v) {
     return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&v), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ __half2 left16(__half2 v, uint32_t codes) {
-    return __hmul2(__hsub2(v, e4m3x2_half2(codes)), __float2half2_rn(16.f));
+__device__ __forceinline__ __half2 left_of(__half2 v, uint32_t codes, float step) {
+    return __hmul2(__hsub2(v, e4m3x2_half2(codes)), __float2half2_rn(step));
+}
+
+// Two fp32 values in one operation.
+struct F2 {
+    unsigned long long b;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 of_f2(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
 }
 
 }  // namespace scaled
@@ -344,7 +385,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 src[it] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * it + r4)) + ch * 16;
             c.advance(p);
             j = entry(c);
-#pragma unroll 1
+#pragma unroll
             for (int s = 0; s < TILES; ++s) {
                 if (!__all_sync(0xffffffffu, wait(B_SLAB_EMPTY + slot, slab_phase))) {
                     abort = true;                            // the whole warp gives up together
@@ -405,8 +446,8 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 for (int s = 0; s < TILES; ++s) {
                     if (!wait_w(B_SLAB_FULL + slot, slab_phase)) break;
                     fence_async_proxy();
-                    umma_e4m3<32, 32>(d, desc_at(DESC_128, base + OFF_SLAB + slot * SLAB),
-                                      desc_at(DESC_128, base + OFF_Q + s * QSLAB), idesc(QROWS, false), s, 4);
+                    umma_e4m3<DESC_128, DESC_128, 32, 32>(d, base + OFF_SLAB + slot * SLAB, base + OFF_Q + s * QSLAB,
+                                                          idesc(QROWS, false), s, 4);
                     if (++slot == SLOTS) {
                         slot = 0;
                         slab_phase ^= 1;
@@ -414,8 +455,8 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 }
                 if (abort || !wait_w(B_ROPE_FULL + rope, rope_phase)) break;
                 fence_async_proxy();
-                umma_e4m3<32, 32>(d, desc_at(DESC_64, base + OFF_ROPE + rope * ROPE),
-                                  desc_at(DESC_64, base + OFF_Q + TILES * QSLAB), idesc(QROWS, false), 1, 2);
+                umma_e4m3<DESC_64, DESC_64, 32, 32>(d, base + OFF_ROPE + rope * ROPE, base + OFF_Q + TILES * QSLAB,
+                                                    idesc(QROWS, false), 1, 2);
                 commit_elected(bar(B_S_FULL + (g & 1)));
                 if (c.last()) commit_elected(bar(B_Q_EMPTY));
                 if (++rope == ROPES) {
@@ -431,12 +472,11 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 if (!wait_w(B_P_FULL + b, (g >> 1) & 1)) break;
                 if (first && !wait_w(B_O_EMPTY, (c.m & 1) ^ 1)) break;
                 tc_fence_after();
-                const uint64_t b0 = desc_at(DESC_P, base + OFF_P + b * PBUF);
                 const uint32_t d = tmem + TM_O;
 #pragma unroll 1
                 for (int t = 0; t < TILES; ++t) {
-                    umma_e4m3<32 * 128, 32 * H>(d + t * OC, desc_at(DESC_128, base + OFF_SLAB + slot * SLAB), b0,
-                                                idesc(OC, true), !first, steps);
+                    umma_e4m3<DESC_128, DESC_P, 32 * 128, 32 * H>(d + t * OC, base + OFF_SLAB + slot * SLAB,
+                                                                  base + OFF_P + b * PBUF, idesc(OC, true), !first, steps);
                     commit_elected(bar(B_SLAB_EMPTY + slot));
                     if (++slot == SLOTS) slot = 0;
                 }
@@ -455,7 +495,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         const float* scales = reinterpret_cast<const float*>(smem + OFF_SCALE);
         const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + hg * HG;
         const int group_bar = SOFTMAX_BAR + hg;
-        float ref[HG], sum[HG], cq[HG];
+        F2 nref[HG / 2], sum[HG / 2], cq[HG / 2];            // minus the references, sums, logit factors
         int rope = 0;
         for (int g = 0; c.valid; ++g, c.advance(p)) {
             const bool first = c.u == 0;
@@ -465,7 +505,20 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             tc_fence_after();
             // (S was issued after its issuer saw the unit's rows, and scales, arrive.)
             const float sv = scales[rope * M + r];
-            float acc[HG];
+            const bool valid = sv > 0.f;
+            const int sexp = (int)(__float_as_uint(sv) >> 23) - 127;
+            if (first) {
+                const float4* q4 = reinterpret_cast<const float4*>(qs + (c.m & 3) * H);
+#pragma unroll
+                for (int q = 0; q < HG / 4; ++q) {
+                    const float4 f = q4[q];
+                    cq[2 * q] = f2(f.x, f.y);
+                    cq[2 * q + 1] = f2(f.z, f.w);
+                }
+#pragma unroll
+                for (int q = 0; q < HG / 2; ++q) nref[q] = sum[q] = f2(0.f, 0.f);
+            }
+            F2 x[HG / 2];                                    // log2 of the row's weights
             {
                 uint32_t d0[8], d1[8], d2[8];
                 const uint32_t at = tmem + lanes + TM_S + (g & 1) * QROWS + hg * HG;
@@ -476,17 +529,12 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 regs_after_wait(d0);
                 regs_after_wait(d1);
                 regs_after_wait(d2);
+                const F2 part = f2(0.0625f, 0.0625f), s2 = f2(sv, sv);
+                const F2 lsv = f2((float)sexp, (float)sexp);     // log2 of the row's scale
+                auto two = [](const uint32_t (&d)[8], int q) { return f2(__uint_as_float(d[2 * q]), __uint_as_float(d[2 * q + 1])); };
 #pragma unroll
-                for (int h = 0; h < HG; ++h)
-                    acc[h] = fmaf(fmaf(__uint_as_float(d2[h]), 0.0625f, __uint_as_float(d1[h])), 0.0625f, __uint_as_float(d0[h]));
-            }
-            if (first) {
-#pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    cq[h] = qs[(c.m & 3) * H + h];
-                    ref[h] = 0.f;
-                    sum[h] = 0.f;
-                }
+                for (int q = 0; q < HG / 2; ++q)
+                    x[q] = fma2(fma2(fma2(two(d2, q), part, two(d1, q)), part, two(d0, q)), mul2(cq[q], s2), lsv);
             }
             tc_fence_before();
             __syncwarp();
@@ -495,21 +543,24 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 mbar_arrive(bar(B_ROPE_EMPTY + rope));
             }
             if (++rope == ROPES) rope = 0;
-            const bool valid = sv > 0.f;
-            const int sexp = (int)(__float_as_uint(sv) >> 23) - 127;
-            const float lsv = (float)sexp;                   // log2 of the row's scale
+            float w[HG];                                     // x - ref, then the weights
             float top = -INFINITY;
+            auto against_ref = [&] {
 #pragma unroll
-            for (int h = 0; h < HG; ++h) {
-                acc[h] = fmaf(acc[h], cq[h] * sv, lsv);      // log2 of the row's weight
-                top = fmaxf(top, acc[h] - ref[h]);
-            }
+                for (int q = 0; q < HG / 2; ++q) {
+                    const float2 d = of_f2(add2(x[q], nref[q]));
+                    w[2 * q] = d.x;
+                    w[2 * q + 1] = d.y;
+                    top = fmaxf(top, fmaxf(d.x, d.y));
+                }
+            };
+            against_ref();
             if (first || named_barrier_or(group_bar, 128, abort || (valid && top > HEADROOM))) {
                 // A new reference: the first unit's maximum, or one raised by this unit.
                 float* red = reinterpret_cast<float*>(smem + OFF_RED) + ((g & 1) * H + hg * HG) * 4;   // [head][quarter]
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
-                    const float mx = warp_max(valid ? acc[h] : -INFINITY);
+                    const float mx = warp_max(valid ? w[h] : -INFINITY);      // above the old reference
                     if (lane == 0) red[4 * h + qd] = mx;
                 }
                 if (named_barrier_or(group_bar, 128, abort)) break;
@@ -518,11 +569,16 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 for (int h = 0; h < HG; ++h) {
                     const float4 m4 = *reinterpret_cast<const float4*>(red + 4 * h);
                     const float mu = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                    const float was = first ? (mu > -INFINITY ? mu + START : 0.f) : ref[h];
-                    ref[h] = mu > was + HEADROOM ? mu + START : was;
-                    alpha[h] = fast_exp2(was - ref[h]);
-                    sum[h] *= alpha[h];
+                    const float up = (first ? mu > -INFINITY : mu > HEADROOM) ? mu + start_of(NT) : 0.f;
+                    alpha[h] = fast_exp2(-up);
+                    w[h] = -up;
                 }
+#pragma unroll
+                for (int q = 0; q < HG / 2; ++q) {
+                    nref[q] = add2(nref[q], f2(w[2 * q], w[2 * q + 1]));
+                    if (!first) sum[q] = mul2(sum[q], f2(alpha[2 * q], alpha[2 * q + 1]));
+                }
+                against_ref();
                 if (!first) {
                     // O^T of the units before has run; this one's waits for the weights below.
                     wait(B_P_EMPTY + ((g - 1) & 1), ((g - 1) >> 1) & 1);
@@ -546,38 +602,41 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     tmem_st_wait();
                 }
             }
-            // Weights, their share of the sums, and their terms.
+            // Weights, their share of the sums, and their terms: w = hi + lo, two fp16 values;
+            // two terms of hi, and NT - 2 of what they leave, lo joining it (NT = 5).
             const float inv = valid ? __uint_as_float((uint32_t)(127 - sexp) << 23) : 0.f;   // 1 / s_r
-#pragma unroll
-            for (int h = 0; h < HG; ++h) {
-                const float w = valid ? fast_exp2(acc[h] - ref[h]) : 0.f;
-                acc[h] = w;
-                sum[h] = fmaf(w, inv, sum[h]);
-            }
-            // w = hi + lo, two fp16 values: three terms of hi, and (NT = 5) two more of what they
-            // leave, of a small hi, and lo, times 16^3.
             uint32_t codes[NT][2];
 #pragma unroll
             for (int q = 0; q < HG / 2; ++q) {
-                uint32_t tc[NT];
-                __half2 v = __floats2half2_rn(acc[2 * q], acc[2 * q + 1]);
-                const float2 hi = __half22float2(v);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t == 3)
-                        v = __hadd2(v, __floats2half2_rn((acc[2 * q] - hi.x) * 4096.f, (acc[2 * q + 1] - hi.y) * 4096.f));
-                    tc[t] = e4m3x2_of(v);
-                    if (t + 1 < NT) v = left16(v, tc[t]);
+                const float wx = valid ? fast_exp2(w[2 * q]) : 0.f, wy = valid ? fast_exp2(w[2 * q + 1]) : 0.f;
+                const F2 w2 = f2(wx, wy);
+                sum[q] = fma2(w2, f2(inv, inv), sum[q]);
+                __half2 v = __floats2half2_rn(wx, wy);
+                F2 lo;
+                if (NT == 5) {
+                    const float2 hi = __half22float2(v);
+                    constexpr float up = term_step(0) * term_step(1);
+                    lo = fma2(f2(hi.x, hi.y), f2(-up, -up), mul2(w2, f2(up, up)));
                 }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) codes[t][q / 2] = q & 1 ? __byte_perm(codes[t][q / 2], tc[t], 0x5410) : tc[t];
+                for (int t = 0; t < NT; ++t) {
+                    if (t == 2 && NT == 5) {
+                        const float2 l2 = of_f2(lo);
+                        v = __hadd2(v, __floats2half2_rn(l2.x, l2.y));
+                    }
+                    const uint32_t tc = e4m3x2_of(v);
+                    if (t + 1 < NT) v = left_of(v, tc, term_step(t));
+                    codes[t][q / 2] = q & 1 ? __byte_perm(codes[t][q / 2], tc, 0x5410) : tc;
+                }
             }
-            const uint32_t prow = base + OFF_P + (g & 1) * PBUF + r * H + hg * (NT - 1) / 2 * (M * H);
+            const uint32_t pbuf = OFF_P + (g & 1) * PBUF + r * H;
 #pragma unroll
             for (int t = 0; t + 1 < NT; t += 2)
-                st_shared_v4(prow + t / 2 * (M * H), make_uint4(codes[t][0], codes[t][1], codes[t + 1][0], codes[t + 1][1]));
-            *reinterpret_cast<uint2*>(smem + OFF_P + (g & 1) * PBUF + r * H + (NT - 1) * (M * H) + hg * HG) =
-                make_uint2(codes[NT - 1][0], codes[NT - 1][1]);
+                st_shared_v4(base + pbuf + o_col<NT>(hg, t) / H * (M * H),
+                             make_uint4(codes[t][0], codes[t][1], codes[t + 1][0], codes[t + 1][1]));
+            if (NT % 2)
+                *reinterpret_cast<uint2*>(smem + pbuf + o_col<NT>(hg, NT - 1) / H * (M * H) + hg * HG) =
+                    make_uint2(codes[NT - 1][0], codes[NT - 1][1]);
             fence_async_proxy();
             tc_fence_before();
             __syncwarp();
@@ -588,11 +647,20 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 __syncwarp();
                 uint32_t bits[8];
 #pragma unroll
-                for (int h = 0; h < HG; ++h) bits[h] = __float_as_uint(sum[h]);
+                for (int q = 0; q < HG / 2; ++q) {
+                    const float2 f = of_f2(sum[q]);
+                    bits[2 * q] = __float_as_uint(f.x);
+                    bits[2 * q + 1] = __float_as_uint(f.y);
+                }
                 tmem_st_x8(tmem + lanes + TM_SUM + (c.m & 1) * H + hg * HG, bits);
                 if (p.split && qd == 0 && lane == 0)
 #pragma unroll
-                    for (int h = 0; h < HG; ++h) reinterpret_cast<float*>(smem + OFF_REF)[(c.m & 1) * H + hg * HG + h] = ref[h];
+                    for (int q = 0; q < HG / 2; ++q) {
+                        const float2 f = of_f2(nref[q]);
+                        float* at = reinterpret_cast<float*>(smem + OFF_REF) + (c.m & 1) * H + hg * HG + 2 * q;
+                        at[0] = -f.x;
+                        at[1] = -f.y;
+                    }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -643,7 +711,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
 #pragma unroll
                         for (int t = 0; t < QT; ++t) {
                             const uint32_t two = e4m3x2_of(v);
-                            if (t + 1 < QT) v = left16(v, two);
+                            if (t + 1 < QT) v = left_of(v, two, 16.f);
                             w[k][t][x / 2] = x & 1 ? __byte_perm(w[k][t][x / 2], two, 0x5410) : two;
                         }
                     }
@@ -740,11 +808,14 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 }
                 float* to = out + h0 * DV + 128 * t + 32 * ew + lane;
 #pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    float v = __uint_as_float(o[NT - 1][h]);
+                for (int h = 0; h < HG; h += 2) {
+                    auto two = [&](int k) { return f2(__uint_as_float(o[k][h]), __uint_as_float(o[k][h + 1])); };
+                    F2 v = two(NT - 1);
 #pragma unroll
-                    for (int k = NT - 2; k >= 0; --k) v = fmaf(v, 0.0625f, __uint_as_float(o[k][h]));
-                    to[h * DV] = v * __shfl_sync(0xffffffffu, mul, h0 + h);
+                    for (int k = NT - 2; k >= 0; --k) v = fma2(v, f2(1.f / term_step(k), 1.f / term_step(k)), two(k));
+                    const float2 f = of_f2(v);
+                    to[h * DV] = f.x * __shfl_sync(0xffffffffu, mul, h0 + h);
+                    to[(h + 1) * DV] = f.y * __shfl_sync(0xffffffffu, mul, h0 + h + 1);
                 }
             }
         }

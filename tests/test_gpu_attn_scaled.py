@@ -8,14 +8,15 @@ left is fp32 sums and the terms of the probabilities. S sums 576 products in fp3
 sum|q k| <= |q| |k|; times scale that is a logit error of 2^-22 * |q| |k| / 24, below 2e-5
 for |q| |k| up to 2,000 (the inputs here: |q| ~ 24, |k| < 80). The exponential adds 2^-22.
 A weight is first hi + lo, hi its fp16 rounding: pv_mode 0 keeps hi alone, off by at most
-2^-11 of the weight (its three terms of four bits hold hi's eleven); pv_mode 1 adds two terms
-of lo, which leave 2^-20. The 640 rows' errors do not add up in phase, but the bound takes
-them as if they did: pv_mode 1 3e-5 (2e-5 + 2^-22 + 2^-20 + sums of 640 in fp32, 2^-24 * 5
-instructions a unit), pv_mode 0 3e-5 + 2^-11 = 5.2e-4, each of sum p |v|, which for cancelling values is larger than
-|out|: both bounds are applied to sum p |v| per element. The last term's smallest spacing is
-2^-9 of its unit, so a row also adds up to 2^-10 / 16^(terms - 1) of |code|, in the unit of
-its weight w = p s / (8 (p s)_max) at least (the largest weight of the first rows is set to
-1/8): over the sum of w / s this is the bound's second part (``floor``), which for a row of
+2^-11 of the weight (its three terms hold hi's eleven bits: a term is off by 2^-4 of itself at
+most, so three leave 2^-12); pv_mode 1 has five, which leave 2^-20. The 640 rows' errors do not
+add up in phase, but the bound takes them as if they did: pv_mode 1 3e-5 (2e-5 + 2^-22 + 2^-20 +
+sums of 640 in fp32, 2^-24 * 4 instructions a unit), pv_mode 0 3e-5 + 2^-11 = 5.2e-4, each of
+sum p |v|, which for cancelling values is larger than |out|: both bounds are applied to
+sum p |v| per element. The last term's smallest spacing is 2^-9 of its unit, 2^-9 (three terms)
+or 2^-18 (five), so a row also adds up to 2^-19 or 2^-28 of |code|, where the largest weight of
+the first rows is set to 1/8 (three terms) or 1/32 (five), so that w is at least p s / (p s)_max
+of that: over the sum of w / s this is the bound's second part (``floor``), which for a row of
 small weight and large values is the larger one.
 """
 import numpy as np
@@ -28,7 +29,7 @@ from sparse_mla_prefill_b200 import ds4sp as D
 
 pytestmark = pytest.mark.gpu
 TOL = {0: 5.2e-4, 1: 3e-5}
-FLOOR = {0: 2.0 ** -15, 1: 2.0 ** -23}
+FLOOR = {0: 2.0 ** -16, 1: 2.0 ** -23}
 
 
 @pytest.fixture(scope="module", autouse=True)
