@@ -127,31 +127,38 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
     }
 }
 
-// mbar_wait for a kernel of many waits that usually miss at first, by a little. The clock and
-// the abort word (a load from global memory, longer than most such waits) are first looked at
-// after 64 tests; and what follows the first test is one function out of line: a kernel whose
-// 25 waits were unrolled had 200 KB of instructions, and its roles spent their time fetching
-// them.
-__device__ __noinline__ bool mbar_wait_out_of_line(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-    unsigned long long t0 = 0;
-#pragma unroll 1
-    for (uint32_t n = 1;; ++n) {
-        if ((n & 63u) == 0 || w.limit_ns == 0) {
-            const unsigned long long now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (launch_gave_up(w) || now - t0 >= w.limit_ns) {
-                give_up(w);
-                return false;
-            }
-        }
-        if (mbar_try_wait(bar, parity)) return true;
-    }
-}
-__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, const WaitCtl& w, bool& abort) {
-    if (abort) return false;
-    if (mbar_test_wait(bar, parity)) return true;
-    abort = !mbar_wait_out_of_line(bar, parity, w);
-    return !abort;
+// mbar_wait for a kernel of many roles and waits, where code size counts (its roles' loops
+// share the instruction caches: with its 25 waits unrolled one kernel had 200 KB of
+// instructions and ran at half its speed): one loop of a dozen instructions. The abort word (a
+// load from global memory, longer than most waits) is looked at from 20 us on. A wait that
+// gives up returns false; its role calls give_up() when it leaves.
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 t0, t;\n\t.reg .b32 v;\n\t"
+        "mov.b32 %0, 1;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t0, %%globaltimer;\n"
+        "AGAIN:\n\t"
+        "mov.u64 t, %%globaltimer;\n\t"
+        "sub.u64 t, t, t0;\n\t"
+        "setp.ge.u64 p, t, %3;\n\t"
+        "@p bra FAIL;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "setp.lt.u64 p, t, 20000;\n\t"
+        "@p bra AGAIN;\n\t"
+        "ld.volatile.global.u32 v, [%4];\n\t"
+        "setp.ne.u32 p, v, %5;\n\t"
+        "@p bra AGAIN;\n"
+        "FAIL:\n\t"
+        "mov.b32 %0, 0;\n"
+        "DONE:\n\t}"
+        : "=&r"(ok)
+        : "r"(bar), "r"(parity), "l"(w.limit_ns), "l"(w.abort_word), "r"(w.epoch)
+        : "memory");
+    return ok != 0;
 }
 
 // Wait for a phase that completes without any other role's help (bulk copies this

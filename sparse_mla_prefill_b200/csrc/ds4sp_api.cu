@@ -704,6 +704,7 @@ ds4sp_status launch_attn(ds4sp_handle* h, const void* q, const void* kv_raw, con
     // and each token's units depend only on the token, so a token's result is the same
     // in every call that takes this path.
     MergeParams mp{};
+    scaled::SplitItems si{};
     p.split = 0;
     p.n_items = n_q;
     if (!tc && n_q <= attn::SPLIT_MAX_TOKENS && h->split_cap > 0) {
@@ -718,7 +719,13 @@ ds4sp_status launch_attn(ds4sp_handle* h, const void* q, const void* kv_raw, con
             fits = fits && nblk <= attn::SPLIT_MAX_UNITS;
         }
         mp.first[n_q] = items;
+        fits = fits && items <= scaled::MAX_SPLIT_ITEMS;
         if (fits && items <= h->split_cap && items > n_q) {
+            for (int i = 0, at = 0; i < n_q; ++i)
+                for (int u = 0; at < mp.first[i + 1]; ++u, ++at) {
+                    si.token[at] = (uint8_t)i;
+                    si.unit[at] = (uint8_t)u;
+                }
             p.split = 1;
             p.n_items = items;
             p.part_o = h->part_o;
@@ -747,9 +754,9 @@ ds4sp_status launch_attn(ds4sp_handle* h, const void* q, const void* kv_raw, con
         } else if (h->cfg.kv_format == kFmtE4M3) {
             const dim3 bsc(scaled::THREADS);
             if (h->cfg.pv_mode == 1)
-                launch_k(pdl, sparse_attn_scaled_kernel<5>, g, bsc, scaled::SMEM_BYTES, stream, p);
+                launch_k(pdl, sparse_attn_scaled_kernel<5>, g, bsc, scaled::SMEM_BYTES, stream, p, si);
             else
-                launch_k(pdl, sparse_attn_scaled_kernel<3>, g, bsc, scaled::SMEM_BYTES, stream, p);
+                launch_k(pdl, sparse_attn_scaled_kernel<3>, g, bsc, scaled::SMEM_BYTES, stream, p, si);
         } else if (h->cfg.kv_format == kFmtQ8) {
             launch_k(pdl, sparse_attn_mma_kernel<false, false, kFmtQ8>, g, bs, smem, stream, p);
         } else if (h->cfg.kv_format == kFmtQ4) {

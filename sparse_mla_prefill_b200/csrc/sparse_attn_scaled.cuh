@@ -200,46 +200,44 @@ struct Item {
     }
 };
 
-// Split mode: items are the 32-row units of token 0, then token 1, ... (out of line: one item
-// per CTA).
-__device__ __noinline__ Item split_item(const AttnParams& p, int idx) {
-    Item it;
-    for (int i = 0;; ++i) {
-        it.of_token(p, i);
-        const int units = (it.rows + SPLIT_ROWS - 1) / SPLIT_ROWS;
-        if (idx < units || i + 1 >= p.n_q) break;
-        idx -= units;
-    }
-    it.row0 = SPLIT_ROWS * idx;
-    it.rows = min(SPLIT_ROWS, it.rows - it.row0);
-    return it;
-}
+// Split mode: item idx is 32-row unit `unit` of token `token` (the units of token 0, then token
+// 1, ...).
+constexpr int MAX_SPLIT_ITEMS = 512;
+struct SplitItems {
+    uint8_t token[MAX_SPLIT_ITEMS], unit[MAX_SPLIT_ITEMS];
+};
+static_assert(attn::SPLIT_MAX_TOKENS <= 256 && attn::SPLIT_MAX_UNITS <= 256, "an item's token and unit are bytes");
 
 // This CTA's units in order: rows [128 u, 128 u + rows()) of its m-th item.
 struct Cursor {
     int m, idx, u;
     Item it;
     bool valid;
-    __device__ __forceinline__ void take(const AttnParams& p) {
+    __device__ __forceinline__ void take(const AttnParams& p, const SplitItems& items) {
         valid = idx < p.n_items;
         u = 0;
         if (!valid) return;
-        if (p.split) it = split_item(p, idx);
-        else it.of_token(p, p.n_q - 1 - idx);                // heaviest (latest) first
+        if (!p.split) {
+            it.of_token(p, p.n_q - 1 - idx);                 // heaviest (latest) first
+            return;
+        }
+        it.of_token(p, items.token[idx]);
+        it.row0 = SPLIT_ROWS * items.unit[idx];
+        it.rows = min(SPLIT_ROWS, it.rows - it.row0);
     }
-    __device__ __forceinline__ void start(const AttnParams& p) {
+    __device__ __forceinline__ void start(const AttnParams& p, const SplitItems& items) {
         m = 0;
         idx = blockIdx.x;
-        take(p);
+        take(p, items);
     }
-    __device__ __forceinline__ void next_item(const AttnParams& p) {
+    __device__ __forceinline__ void next_item(const AttnParams& p, const SplitItems& items) {
         ++m;
         idx += gridDim.x;
-        take(p);
+        take(p, items);
     }
     __device__ __forceinline__ bool last() const { return M * (u + 1) >= it.rows; }
-    __device__ __forceinline__ void advance(const AttnParams& p) {
-        if (last()) next_item(p);
+    __device__ __forceinline__ void advance(const AttnParams& p, const SplitItems& items) {
+        if (last()) next_item(p, items);
         else ++u;
     }
     __device__ __forceinline__ int rows() const { return min(M, it.rows - M * u); }
@@ -287,7 +285,8 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 }  // namespace scaled
 
 template <int NT>
-__global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(scaled::THREADS, 1)
+sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ scaled::SplitItems items) {
     using namespace scaled;
     constexpr int OC = o_cols<NT>(), PBUF = NT * M * H;
     extern __shared__ uint8_t smem_raw[];
@@ -334,9 +333,12 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
     grid_dependents_launch();
 
     bool abort = false;
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait_soon(bar(b), parity, p.wc, abort); };
+    auto wait = [&](int b, uint32_t parity) {
+        if (!abort) abort = !mbar_wait_small(bar(b), parity, p.wc);
+        return !abort;
+    };
     Cursor c;
-    c.start(p);
+    c.start(p, items);
 
     if (warp >= PWARP0 && warp < SMMA) {
         // ================================================================ gather
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
 #pragma unroll
             for (int it = 0; it < 8; ++it)
                 src[it] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * it + r4)) + ch * 16;
-            c.advance(p);
+            c.advance(p, items);
             j = entry(c);
 #pragma unroll
             for (int s = 0; s < TILES; ++s) {
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         if (warp == SMMA) {                                  // S of each unit
             int slot = 0, rope = 0;
             uint32_t slab_phase = 0, rope_phase = 0;
-            for (int g = 0; c.valid && !abort; ++g, c.advance(p)) {
+            for (int g = 0; c.valid && !abort; ++g, c.advance(p, items)) {
                 if (c.u == 0 && !wait_w(B_Q_FULL, c.m & 1)) break;
                 if (!wait_w(B_S_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1)) break;
                 tc_fence_after();
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             }
         } else {                                             // O^T
             int slot = 0;
-            for (int g = 0; c.valid && !abort; ++g, c.advance(p)) {
+            for (int g = 0; c.valid && !abort; ++g, c.advance(p, items)) {
                 const int b = g & 1, steps = (c.rows() + 31) / 32;
                 const bool first = c.u == 0;
                 if (!wait_w(B_P_FULL + b, (g >> 1) & 1)) break;
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         const int group_bar = SOFTMAX_BAR + hg;
         F2 nref[HG / 2], sum[HG / 2], cq[HG / 2];            // minus the references, sums, logit factors
         int rope = 0;
-        for (int g = 0; c.valid; ++g, c.advance(p)) {
+        for (int g = 0; c.valid; ++g, c.advance(p, items)) {
             const bool first = c.u == 0;
             wait(B_P_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1);   // O^T of the unit before last: its weights
             wait(B_S_FULL + (g & 1), (g >> 1) & 1);
@@ -694,11 +696,15 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                         for (int x = 0; x < 4; ++x) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&u[x])));
                     }
                 }
-                float top = fminf(fmaxf(__low2float(top2), __high2float(top2)), 65504.f);
+                float top = fmaxf(__low2float(top2), __high2float(top2));
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const int e = max(scale_exponent(top), -30);         // 2^30 is two fp16 factors
-                const __half2 up0 = __float2half2_rn(pow2f(-e / 2)), up1 = __float2half2_rn(pow2f(-e - -e / 2));
+                // (2^15 is fp16's largest power of two: it makes whole steps of the first term of
+                // fp16's smallest values, so nothing is lost there. An infinity makes the head's
+                // factor NaN.)
+                const int e = max(scale_exponent(fminf(top, 65504.f)), -15);
+                const __half2 up = __float2half2_rn(pow2f(-e));
+                const float factor = top < INFINITY ? pow2f(e) * p.scale_log2 : NAN;
                 uint32_t w[9][QT][2];
 #pragma unroll
                 for (int k = 0; k < 9; ++k) {
@@ -706,8 +712,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                     const uint32_t u[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u[x]), up0), up1);
-                        v = __hfma2(v, __float2half2_rn(0.f), v);    // an infinity becomes NaN
+                        __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&u[x]), up);
 #pragma unroll
                         for (int t = 0; t < QT; ++t) {
                             const uint32_t two = e4m3x2_of(v);
@@ -718,7 +723,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
                 }
                 if (have) wait(B_Q_EMPTY, om & 1);           // (a wait that gave up: all stop below)
                 __syncwarp();
-                if (ql == 0) reinterpret_cast<float*>(smem + OFF_QS)[(c.m & 3) * H + qh] = pow2f(e) * p.scale_log2;
+                if (ql == 0) reinterpret_cast<float*>(smem + OFF_QS)[(c.m & 3) * H + qh] = factor;
                 // dims 64k + 8ql ..: half a 16-byte chunk of row t * 16 + qh (whose swizzles are
                 // qh's, t * 16 being whole atoms). Odd heads take k ^ 1, so that a warp's four
                 // heads cover both halves of the banks.
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
             om = c.m;
             oi = c.it.i;
             oidx = c.idx;
-            if (c.valid) c.next_item(p);
+            if (c.valid) c.next_item(p, items);
             if (!output) continue;
             wait(B_L_FULL + (m & 1), (m >> 1) & 1);
             __syncwarp();
@@ -821,6 +826,7 @@ __global__ void __launch_bounds__(scaled::THREADS, 1) sparse_attn_scaled_kernel(
         }
     }
 
+    if (abort) give_up(p.wc);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
