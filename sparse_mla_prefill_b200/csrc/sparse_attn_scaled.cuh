@@ -82,7 +82,7 @@ constexpr int B_SLAB_FULL = 0, B_SLAB_EMPTY = B_SLAB_FULL + SLOTS, B_ROPE_FULL =
               B_ROPE_EMPTY = B_ROPE_FULL + ROPES, B_Q_FULL = B_ROPE_EMPTY + ROPES, B_Q_EMPTY = B_Q_FULL + 1,
               B_S_FULL = B_Q_EMPTY + 1, B_S_EMPTY = B_S_FULL + 2, B_P_FULL = B_S_EMPTY + 2,
               B_P_EMPTY = B_P_FULL + 2, B_O_FULL = B_P_EMPTY + 2, B_O_EMPTY = B_O_FULL + 1,
-              B_L_FULL = B_O_EMPTY + 1, B_L_EMPTY = B_L_FULL + 2, B_DONE = B_L_EMPTY + 2, N_BARS = B_DONE + 1;
+              B_L_FULL = B_O_EMPTY + TILES, B_L_EMPTY = B_L_FULL + 2, B_DONE = B_L_EMPTY + 2, N_BARS = B_DONE + 1;
 constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;             // + alignment slack
 static_assert(OFF_ROPE % 1024 == 0 && OFF_Q % 1024 == 0 && QSLAB % 1024 == 0 && OFF_P % 128 == 0 && OFF_BAR % 8 == 0,
@@ -309,7 +309,7 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
         mbar_init(bar(B_Q_FULL), EWARPS);
         mbar_init(bar(B_Q_EMPTY), 1);
         mbar_init(bar(B_O_FULL), 1);
-        mbar_init(bar(B_O_EMPTY), EWARPS);
+        for (int t = 0; t < TILES; ++t) mbar_init(bar(B_O_EMPTY + t), EWARPS);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_S_FULL + i), 1);
             mbar_init(bar(B_S_EMPTY + i), SWARPS);
@@ -472,16 +472,18 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 const int b = g & 1, steps = (c.rows() + 31) / 32;
                 const bool first = c.u == 0;
                 if (!wait_w(B_P_FULL + b, (g >> 1) & 1)) break;
-                if (first && !wait_w(B_O_EMPTY, (c.m & 1) ^ 1)) break;
-                tc_fence_after();
                 const uint32_t d = tmem + TM_O;
 #pragma unroll 1
                 for (int t = 0; t < TILES; ++t) {
+                    // (a token's first unit overwrites tile by tile, behind the output's reads)
+                    if (first && !wait_w(B_O_EMPTY + t, (c.m & 1) ^ 1)) break;
+                    tc_fence_after();
                     umma_e4m3<DESC_128, DESC_P, 32 * 128, 32 * H>(d + t * OC, base + OFF_SLAB + slot * SLAB,
                                                                   base + OFF_P + b * PBUF, idesc(OC, true), !first, steps);
                     commit_elected(bar(B_SLAB_EMPTY + slot));
                     if (++slot == SLOTS) slot = 0;
                 }
+                if (abort) break;
                 commit_elected(bar(B_P_EMPTY + b));
                 if (c.last()) commit_elected(bar(B_O_FULL));
             }
@@ -681,20 +683,21 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 // The terms of the next item's queries into shared memory, once the last S of
                 // the item before has read its own; and the heads' logit factors.
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)c.it.i * H + qh) * DQK);
-                // (two passes over the head's values, the second from cache: its largest, then
-                // the terms, which wait in registers)
+                uint4 qv[9];
                 __half2 top2 = __float2half2_rn(0.f);
-#pragma unroll 1
-                for (int k3 = 0; k3 < 9; k3 += 3) {
-                    uint4 qv[3];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) qv[k] = __ldg(src + 8 * (k3 + k) + ql);
+                for (int k = 0; k < 9; ++k) qv[k] = __ldg(src + 8 * (k < 8 ? k ^ (qh & 1) : k) + ql);
+                if (c.idx + (int)gridDim.x < p.n_items && !p.split) {
+                    // The item after it: its queries, read once, come from memory.
+                    const char* nx = reinterpret_cast<const char*>(p.q + (size_t)(c.it.i - (int)gridDim.x) * H * DQK);
+                    for (int at = et * 128; at < H * DQK * 2; at += EWARPS * 32 * 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + at));
+                }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+                for (int k = 0; k < 9; ++k) {
+                    const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&u[x])));
-                    }
+                    for (int x = 0; x < 4; ++x) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __half2*>(&u[x])));
                 }
                 float top = fmaxf(__low2float(top2), __high2float(top2));
 #pragma unroll
@@ -708,8 +711,7 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 uint32_t w[9][QT][2];
 #pragma unroll
                 for (int k = 0; k < 9; ++k) {
-                    const uint4 qv = __ldg(src + 8 * (k < 8 ? k ^ (qh & 1) : k) + ql);
-                    const uint32_t u[4] = {qv.x, qv.y, qv.z, qv.w};
+                    const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&u[x]), up);
@@ -793,22 +795,28 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 p.part_ml[(size_t)oidx_ * 2 * H + hl] = ref;
                 p.part_ml[(size_t)oidx_ * 2 * H + H + hl] = L;
             }
-            // Eight heads of a tile at a time.
+            // A tile at a time, eight heads at a time.
+            F2 by[H / 2];
+#pragma unroll
+            for (int h = 0; h < H; h += 2)
+                by[h / 2] = f2(__shfl_sync(0xffffffffu, mul, h), __shfl_sync(0xffffffffu, mul, h + 1));
 #pragma unroll 1
-            for (int part = 0; part < 2 * TILES; ++part) {
-                const int t = part >> 1, h0 = (part & 1) * HG;
+            for (int t = 0; t < TILES; ++t) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int h0 = half * HG;
                 uint32_t o[NT][8];
 #pragma unroll
-                for (int k = 0; k < NT; ++k) tmem_ld_x8(tmem + lanes + TM_O + t * OC + o_col<NT>(part & 1, k), o[k]);
+                for (int k = 0; k < NT; ++k) tmem_ld_x8(tmem + lanes + TM_O + t * OC + o_col<NT>(half, k), o[k]);
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < NT; ++k) regs_after_wait(o[k]);
-                if (part + 1 == 2 * TILES) {                 // O^T and the sums are read
+                if (half == 1) {                             // the tile is read (and the sums)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(bar(B_O_EMPTY));
-                        mbar_arrive(bar(B_L_EMPTY + (m & 1)));
+                        mbar_arrive(bar(B_O_EMPTY + t));
+                        if (t + 1 == TILES) mbar_arrive(bar(B_L_EMPTY + (m & 1)));
                     }
                 }
                 float* to = out + h0 * DV + 128 * t + 32 * ew + lane;
@@ -818,10 +826,11 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     F2 v = two(NT - 1);
 #pragma unroll
                     for (int k = NT - 2; k >= 0; --k) v = fma2(v, f2(1.f / term_step(k), 1.f / term_step(k)), two(k));
-                    const float2 f = of_f2(v);
-                    to[h * DV] = f.x * __shfl_sync(0xffffffffu, mul, h0 + h);
-                    to[(h + 1) * DV] = f.y * __shfl_sync(0xffffffffu, mul, h0 + h + 1);
+                    const float2 f = of_f2(mul2(v, by[(h0 + h) / 2]));
+                    to[h * DV] = f.x;
+                    to[(h + 1) * DV] = f.y;
                 }
+              }
             }
         }
     }
