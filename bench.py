@@ -653,6 +653,8 @@ VARIANTS = [
     ("q8_0_cache", dict(kv_format=1)),
     ("q4_0_cache", dict(kv_format=2)),
     ("q8k_q4v_cache", dict(kv_format=3)),
+    ("e4m3_block_cache", dict(kv_format=5)),
+    ("e4m3_block_cache_fp32_staged", dict(kv_format=5, pv_mode=1)),
 ]
 
 
@@ -678,9 +680,9 @@ def main():
     ap.add_argument("--attn-kernel", type=int, default=0, choices=[0, 1],
                     help="the headline step's attention kernel (1 = logits on tcgen05; for "
                          "profiling; the default line uses 0)")
-    ap.add_argument("--kv-format", type=int, default=0, choices=[0, 1, 2, 3],
+    ap.add_argument("--kv-format", type=int, default=0, choices=[0, 1, 2, 3, 5],
                     help="the headline step's cache format (1 = Q8_0, 2 = Q4_0, 3 = Q8 K / "
-                         "Q4 V; for profiling; the default line uses fp16 rows)")
+                         "Q4 V, 5 = e4m3 with a scale per block; for profiling; the default line uses fp16 rows)")
     args = ap.parse_args()
     if args.warmup < 3:
         ap.error("--warmup must be >= 3")

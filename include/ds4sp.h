@@ -25,7 +25,8 @@
  *     pointer is 16-byte aligned. fp16 means IEEE binary16; fp32 means IEEE binary32.
  *   - Per-token tensors (q, q_idx, w, topk, out) start at token t0: row 0 is token t0.
  *     KV tensors (kv_raw, kv_cmp, k_idx) are whole-sequence base pointers holding at
- *     least max_tokens (raw) or max_tokens/4 (compressed) rows.
+ *     least max_tokens (raw) or max_tokens/4 (compressed) rows (kv_format 5: whole blocks,
+ *     ds4sp_cache_bytes of them).
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *     stream). The library launches kernels only; it never allocates or frees caller
  *     memory, copies it only in ds4sp_prefill_host (between the caller's host and
@@ -346,8 +347,9 @@ ds4sp_status ds4sp_indexer_topk_noalloc(const ds4sp_config* cfg, const void* q_i
  * ds4sp_kv_row_bytes: bytes of one stored row of `dims` values (a multiple of 32, at most
  * 4096; at least 512 for format 3) in kv_format 1, 2 or 3, or 0 for anything else.
  * ds4sp_quantize_kv: quantize x [rows, dims] fp16 (device) into out [rows,
- * ds4sp_kv_row_bytes(kv_format, dims)] bytes (device, caller-owned). Asynchronous on
- * `stream`; argument errors are returned before the launch. */
+ * ds4sp_kv_row_bytes(kv_format, dims)] bytes (device, caller-owned), or in kv_format 5 into
+ * a cache of ds4sp_cache_bytes(5, dims, rows) bytes (ds4sp_cache_write of all rows).
+ * Asynchronous on `stream`; argument errors are returned before the launch. */
 int ds4sp_kv_row_bytes(int kv_format, int dims);
 ds4sp_status ds4sp_quantize_kv(const void* x, int rows, int dims, int kv_format, void* out,
                                void* stream);
@@ -411,7 +413,8 @@ ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype
  * multiple of 8), 1 .. 3 (as for ds4sp_kv_row_bytes), 5 (a multiple of 16; whole blocks are
  * counted); at most 4096 values, 0 for anything else.
  *
- * ds4sp_cache_write: store x [n, dims] (dtype, rows x_stride values apart) as rows row0 ..
+ * ds4sp_cache_write: store x [n, dims] (dtype, rows x_stride values apart; finite values of
+ * fp16's range in kv_format 0 .. 3) as rows row0 ..
  * row0+n-1 of the cache of cache_rows rows. rope (may be NULL) turns part of each row first;
  * the turned values are rounded only by the cache's format. positions, pos0 and pos_step as
  * for ds4sp_rope. In kv_format 5 a write that starts inside a block (row0 % 64 != 0) appends

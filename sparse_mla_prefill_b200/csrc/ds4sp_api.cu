@@ -1464,6 +1464,8 @@ int ds4sp_kv_row_bytes(int kv_format, int dims) {
 ds4sp_status ds4sp_quantize_kv(const void* x, int rows, int dims, int kv_format, void* out,
                                void* stream) {
     const TraceRange trace("ds4sp_quantize_kv");
+    if (kv_format == kFmtE4M3)
+        return ds4sp_cache_write(out, kv_format, dims, rows, 0, rows, x, DS4SP_F16, dims, nullptr, nullptr, 0, 0, stream);
     const int rb = ds4sp_kv_row_bytes(kv_format, dims);
     if (rb == 0)
         return fail(DS4SP_ERR_INVALID_ARG, "kv_format %d with %d dims (1 = Q8_0 or 2 = Q4_0, "

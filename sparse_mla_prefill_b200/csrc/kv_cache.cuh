@@ -345,7 +345,7 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
     __shared__ float warp_top[kE4M3Threads / 32];
     const int tid = threadIdx.x, r = tid / 8, l = tid % 8;
     const int blk = p.row0 / kScaleBlock + blockIdx.x;
-    const int i = blk * kScaleBlock + r - p.row0;        // this lane's row of the written ones
+    const int i = (int)((long long)blk * kScaleBlock + r - p.row0);      // this lane's row of the written ones
     const bool in = i >= 0 && i < p.n;
     const int chunks = p.dims / 8;
     uint8_t* base = cache + (long long)blk * (kScaleBlock + 1) * p.dims;

@@ -136,7 +136,7 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None) -> Optional[int]:
 
 
 def _kv_dtype(t) -> torch.dtype:
-    """KV tensors are fp16 rows, or uint8 rows of a quantized cache (kv_format 1, 2)."""
+    """KV tensors are fp16 rows, or the uint8 rows of a quantized cache."""
     return torch.uint8 if t is not None and t.dtype == torch.uint8 else torch.float16
 
 
@@ -182,7 +182,8 @@ def make_config(n_idx_heads: int, d_idx: int, top_k: int, n_swa: int, max_tokens
     kernel, where it measured faster; else 0); pv_mode: 0 = fp16 probabilities in P . V, 1 = fp32-staged (hi + lo fp16);
     topk_mode: 1 (the default) = fused indexer + top-k where the call qualifies, 0 =
     scores in the workspace and a separate top-k kernel; kv_format: 0 = fp16 KV rows, 1 = Q8_0,
-    2 = Q4_0, 3 = Q8 K / Q4 V quantized rows (ds4sp_quantize_kv); dependent_launch:
+    2 = Q4_0, 3 = Q8 K / Q4 V quantized rows (ds4sp_quantize_kv), 5 = e4m3 rows with a scale
+    per block of 64 (ds4sp_cache_write); dependent_launch:
     1 = each kernel a programmatic dependent of the one before it, 0 = plain order;
     attn_kernel: 0 = mma.sync streaming attention, 1 = logits on tcgen05 (TMEM);
     indexer_kernel: 0 = one CTA per tcgen05 tile, 1 = CTA pairs sharing each MMA."""
@@ -233,8 +234,23 @@ def ds4sp_indexer_topk_noalloc(cfg: ds4sp_config, q_idx, k_idx, w, t0: int, n_q:
            "ds4sp_indexer_topk_noalloc")
 
 
+def _check_blocks(h: Handle, kv_raw, kv_cmp, tokens: int) -> None:
+    """kv_format 5: caches that hold the rows a call reaches (a block's scale lies behind its
+    rows, so a tensor of plain rows would pass for one)."""
+    if h.cfg.kv_format != 5:
+        return
+    for t, name, rows in ((kv_raw, "kv_raw", tokens), (kv_cmp, "kv_cmp", tokens // h.cfg.ratio if h.cfg.top_k else 0)):
+        if t is not None and rows > 0 and (t.dtype != torch.uint8 or _cache_rows(t.numel()) < rows):
+            raise Ds4spError(ERR_INVALID_ARG, name, f"expected a uint8 kv_format 5 cache of {rows} rows or more")
+
+
+def _cache_rows(nbytes: int, dims: int = 576) -> int:
+    return nbytes // ((SCALE_BLOCK + 1) * dims) * SCALE_BLOCK
+
+
 def ds4sp_sparse_attn(h: Handle, q, kv_raw, kv_cmp, topk, t0: int, n_q: int, out, stream=None):
     lib = load_library()
+    _check_blocks(h, kv_raw, kv_cmp, t0 + n_q)
     _check(lib.ds4sp_sparse_attn(h.ptr, _ptr(q, "q", torch.float16),
                                  _ptr(kv_raw, "kv_raw", _kv_dtype(kv_raw)),
                                  _ptr(kv_cmp, "kv_cmp", _kv_dtype(kv_cmp)),
@@ -246,6 +262,7 @@ def ds4sp_sparse_attn(h: Handle, q, kv_raw, kv_cmp, topk, t0: int, n_q: int, out
 def ds4sp_prefill_band(h: Handle, b: int, n_tokens: int, q, q_idx, w, kv_raw, kv_cmp, k_idx,
                        topk, out, ws, stream=None):
     lib = load_library()
+    _check_blocks(h, kv_raw, kv_cmp, min((b + 1) * h.cfg.band, n_tokens))
     _check(lib.ds4sp_prefill_band(h.ptr, b, n_tokens, _ptr(q, "q", torch.float16),
                                   _ptr(q_idx, "q_idx", torch.float16),
                                   _ptr(w, "w", torch.float32),
@@ -319,9 +336,12 @@ def ds4sp_kv_row_bytes(kv_format: int, dims: int) -> int:
 
 def ds4sp_quantize_kv(x, kv_format: int, out=None, stream=None):
     """Quantize fp16 rows x [rows, dims] (device) into the stored row layout; returns
-    ``out`` (uint8 [rows, ds4sp_kv_row_bytes(kv_format, dims)], allocated if None)."""
+    ``out`` (uint8 [rows, ds4sp_kv_row_bytes(kv_format, dims)], or for kv_format 5 a cache of
+    ds4sp_cache_bytes(5, dims, rows) bytes; allocated if None)."""
     rows, dims = x.shape
     rb = ds4sp_kv_row_bytes(kv_format, dims)
+    if out is None and kv_format == 5:
+        out = torch.empty(max(ds4sp_cache_bytes(5, dims, rows), 16), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((rows, max(rb, 16)), dtype=torch.uint8, device=x.device)
     _check(load_library().ds4sp_quantize_kv(_ptr(x, "x", torch.float16), rows, dims, kv_format,
@@ -509,6 +529,8 @@ def ds4sp_prefill_host(h: Handle, n_tokens: int, host: Dict[str, torch.Tensor],
                        dev: Dict[str, torch.Tensor], dev_topk: Optional[torch.Tensor],
                        dev_out: torch.Tensor, ws: Optional[torch.Tensor], stream=None) -> None:
     lib = load_library()
+    for side in (host, dev):
+        _check_blocks(h, side["kv_raw"], side.get("kv_cmp"), n_tokens)
     hio, dio = _io(host, host_topk, host_out, True), _io(dev, dev_topk, dev_out, False)
     _check(lib.ds4sp_prefill_host(h.ptr, n_tokens, ctypes.byref(hio), ctypes.byref(dio),
                                   _ptr(ws, "ws"),

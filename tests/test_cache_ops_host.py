@@ -153,3 +153,26 @@ def test_binding_refuses_host_tensors(lib):
         D.ds4sp_cache_write(torch.zeros(65 * 576, dtype=torch.uint8), 5, torch.zeros(1, 576), 0)
     with pytest.raises(D.Ds4spError):
         D.ds4sp_cache_read(torch.zeros(65 * 576, dtype=torch.uint8), 5, 576)
+
+
+@pytest.mark.parametrize("kw", [dict(exp_mode=1), dict(exp_mode=1, pv_mode=1), dict(attn_kernel=1),
+                                dict(attn_kernel=1, pv_mode=1)])
+def test_create_refuses_what_a_scaled_cache_has_not(lib, kw):
+    cfg = D.make_config(16, 64, 64, 32, 1024, kv_format=5, **kw)
+    out = ctypes.c_void_p(123)
+    assert lib.ds4sp_create(ctypes.byref(cfg), ctypes.byref(out)) == D.ERR_UNSUPPORTED
+    assert out.value is None and lib.ds4sp_last_error()
+
+
+@pytest.mark.parametrize("rows,ok", [(0, False), (1, True), (64, True), (65, True)])
+def test_binding_asks_for_whole_blocks(rows, ok):
+    """70 tokens (two blocks) and their 17 compressed rows (one), against a cache of `rows` rows."""
+    h = D.Handle(0, D.make_config(16, 64, 64, 32, 1024, kv_format=5))
+    two = torch.zeros(D.ds4sp_cache_bytes(5, 576, 70), dtype=torch.uint8)
+    some = torch.zeros(D.ds4sp_cache_bytes(5, 576, rows), dtype=torch.uint8)
+    plain = torch.zeros(70, 576, dtype=torch.uint8)
+    D._check_blocks(h, two, some if ok else None, 70)
+    refused = [(plain, two), (plain.half(), two)] + ([] if ok else [(two, some)]) + ([] if rows > 64 else [(some, two)])
+    for raw, cmp in refused:
+        with pytest.raises(D.Ds4spError):
+            D._check_blocks(h, raw, cmp, 70)

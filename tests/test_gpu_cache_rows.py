@@ -252,3 +252,19 @@ def test_captured_append_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert not torch.equal(out, want) and torch.equal(out, read(cache, row0=0, n=65))
+
+
+@pytest.mark.parametrize("rows,dims", [(0, 576), (1, 576), (63, 64), (64, 576), (200, 576), (129, 2048)])
+def test_quantizer_writes_the_scaled_cache(rows, dims):
+    """ds4sp_quantize_kv in kv_format 5 is a write of fp16 rows from row 0 on: the same bytes."""
+    x = rows_of(rows, dims, 21)
+    want = torch.zeros(D.ds4sp_cache_bytes(5, dims, rows), dtype=torch.uint8, device="cuda")
+    if rows:
+        D.ds4sp_cache_write(want, 5, x, 0)
+    out = torch.zeros(max(want.numel(), 16), dtype=torch.uint8, device="cuda")
+    assert D.ds4sp_quantize_kv(x, 5, out=out) is out
+    assert torch.equal(out[: want.numel()], want)
+    fresh = D.ds4sp_quantize_kv(x, 5)
+    assert fresh.dim() == 1 and fresh.numel() >= want.numel()
+    if rows:
+        assert torch.equal(read(fresh, dims, n=rows), read(want, dims, n=rows))
