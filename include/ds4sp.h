@@ -377,7 +377,7 @@ typedef struct {
     int layout;          /* 0 = interleaved pairs, 1 = halves */
     int scaling;         /* 0 none, 1 linear, 2 NTK, 3 YaRN */
     double base;         /* > 1 */
-    double factor;       /* > 0 (scaling 1-3); ignored without scaling */
+    double factor;       /* > 0, large enough for finite f_i (scaling 1-3); ignored without scaling */
     int orig_len;        /* >= 1 (scaling 3): the context the model was trained at */
     double beta_fast;    /* scaling 3: turns over orig_len; <= 0 selects 32 */
     double beta_slow;    /* likewise; <= 0 selects 1 */
@@ -387,8 +387,9 @@ typedef struct {
 /* Turn the rotary part of x [n_tokens, heads, head_dim] into out (the attention takes its
  * queries and rows after rotation). Token and head strides are in values; the values of a
  * head are contiguous, at the alignment of their type (16-byte aligned rows are faster).
- * The head's other values are copied; head_dim is at most 2^20. out may be x with the same strides (in place);
- * otherwise the two must not share elements, and out's heads must not overlap one another.
+ * The head's other values are copied; head_dim is at most 2^20, heads 2^30. out may be x
+ * with the same strides (in place); otherwise the two must not share elements, and out's
+ * heads must not overlap one another.
  *   positions  [n_tokens] int32 (device), or NULL: row i is at pos0 + i * pos_step (raw
  *              rows: the token and 1; compressed row j: 4 * j and 4)
  *   transpose  1: the transposed rotation, the gradient of this function (its inverse
@@ -432,7 +433,8 @@ ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype
  *
  * Both are asynchronous on `stream`; argument errors are returned before the launch. The
  * cache is 16-byte aligned; x and out need the alignment of their type (16-byte aligned rows
- * are faster). The pointers belong to the current device. */
+ * are faster) and share no bytes with the cache, nor out's rows with one another. The
+ * pointers belong to the current device. */
 size_t ds4sp_cache_bytes(int kv_format, int dims, long long rows);
 ds4sp_status ds4sp_cache_write(void* cache, int kv_format, int dims, int cache_rows, int row0, int n,
                                const void* x, ds4sp_dtype dtype, long long x_stride,

@@ -934,7 +934,7 @@ ds4sp_status make_rope_table(const ds4sp_rope_config* cfg, RopeTable* tab) {
         return fail(DS4SP_ERR_INVALID_ARG, "rotary factor %g (> 0)", c.factor);
     if (c.scaling == 2 && c.dims < 4) return fail(DS4SP_ERR_INVALID_ARG, "NTK scaling needs 4 rotary dims");
     if (c.scaling == 3 && c.orig_len < 1) return fail(DS4SP_ERR_INVALID_ARG, "YaRN orig_len %d (>= 1)", c.orig_len);
-    if (std::isnan(c.beta_fast) || std::isnan(c.beta_slow) || std::isnan(c.mscale) || std::isinf(c.mscale))
+    if (std::isnan(c.beta_fast) || std::isnan(c.beta_slow) || !std::isfinite((float)c.mscale))
         return fail(DS4SP_ERR_INVALID_ARG, "rotary beta_fast, beta_slow or mscale is not a number");
     constexpr double kTwoPi = 6.283185307179586476925286766559;
     const double d = c.dims, s = c.scaling == 0 ? 1.0 : c.factor;
@@ -955,6 +955,7 @@ ds4sp_status make_rope_table(const ds4sp_rope_config* cfg, RopeTable* tab) {
             const double r = std::min(std::max((i - low) / (high - low), 0.0), 1.0);
             f = f / s * r + f * (1.0 - r);
         }
+        if (!std::isfinite(f)) return fail(DS4SP_ERR_INVALID_ARG, "rotary factor %g leaves pair %d no frequency", s, i);
         // In turns, modulo one (a factor below 1/2pi makes a step of more than a turn):
         // 32 bits at a time, since a 64-bit fraction does not fit a double's mantissa.
         const double turns = f / kTwoPi, frac = turns - std::floor(turns);
@@ -1508,7 +1509,7 @@ ds4sp_status ds4sp_rope(const ds4sp_rope_config* cfg, const void* x, ds4sp_dtype
     DS4SP_TRY(rope_table(cfg, transpose, &p.tab));
     const int es = dtype_bytes(dtype);
     if (es == 0) return fail(DS4SP_ERR_INVALID_ARG, "dtype %d", (int)dtype);
-    if (n_tokens < 0 || heads < 1 || head_dim < 1 || head_dim > (1 << 20))
+    if (n_tokens < 0 || heads < 1 || heads > (1 << 30) || head_dim < 1 || head_dim > (1 << 20))
         return fail(DS4SP_ERR_INVALID_ARG, "n_tokens %d, heads %d, head_dim %d", n_tokens, heads, head_dim);
     if ((long long)cfg->offset + cfg->dims > head_dim)
         return fail(DS4SP_ERR_INVALID_ARG, "rotary dims [%d, %d) of a head of %d", cfg->offset,

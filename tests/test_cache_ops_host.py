@@ -99,6 +99,18 @@ def test_rope_refuses_configurations(lib, kw):
     assert lib.ds4sp_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(scaling=1, factor=1e-309), dict(scaling=2, factor=1e-318),
+                                dict(scaling=3, factor=1e-309, orig_len=4096), dict(mscale=1e300)])
+def test_rope_refuses_frequencies_and_magnitudes_out_of_range(lib, kw):
+    assert _rope(lib, D.make_rope(64, **kw)) == D.ERR_INVALID_ARG
+    assert lib.ds4sp_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(heads=(1 << 30) + 1), dict(head=(1 << 20) + 1, os_=(1 << 22, 1 << 21))])
+def test_rope_refuses_sizes(lib, kw):
+    assert _rope(lib, D.make_rope(64), **kw) == D.ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("kw", [dict(x=None), dict(out=None), dict(x=P + 1), dict(dtype=2, out=P + 2), dict(dtype=3),
                                 dict(n=-1), dict(heads=0), dict(head=0), dict(xs=(-1, 64)), dict(os_=(63, 64)),
                                 dict(os_=(128, 63)), dict(pos=P + 2)])
