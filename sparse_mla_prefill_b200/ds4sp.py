@@ -367,27 +367,28 @@ def make_rope(dims: int, offset: int = 0, layout: int = 0, base: float = 10000.0
 
 def _device() -> int:
     """The current CUDA device, which host tensors (device -1) are not on."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
-def _rows(t: torch.Tensor, name: str, dims: int) -> int:
-    """The dtype code of a strided device tensor of `dims` dimensions whose last one is
-    contiguous. It belongs to the current device, whose stream the call uses."""
-    if t.get_device() != _device():
-        raise Ds4spError(ERR_INVALID_ARG, name, "tensor must be on the current CUDA device")
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise Ds4spError(ERR_INVALID_ARG, name, f"expected {dims} dimensions, the last one contiguous")
+def _stream_on(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows(t: torch.Tensor, name: str, dims: int, dev: int) -> int:
+    """The dtype code of a strided tensor of `dims` dimensions whose last one is contiguous, on
+    the current device, whose stream the call uses."""
     code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise Ds4spError(ERR_INVALID_ARG, name, f"dtype {t.dtype}, expected float16, bfloat16 or float32")
+    if t.get_device() != dev or t.dim() != dims or code is None or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise Ds4spError(ERR_INVALID_ARG, name, f"expected a float16, bfloat16 or float32 tensor of {dims} "
+                         "dimensions, the last one contiguous, on the current CUDA device; got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
     return code
 
 
-def _int_rows(t: Optional[torch.Tensor], name: str, n: int) -> Optional[int]:
+def _int_rows(t: Optional[torch.Tensor], name: str, n: int, dev: int) -> Optional[int]:
     if t is None:
         return None
-    if t.get_device() != _device() or t.dtype != torch.int32 \
-            or not t.is_contiguous() or t.numel() != n:
+    if t.get_device() != dev or t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
         raise Ds4spError(ERR_INVALID_ARG, name, f"expected a contiguous int32 tensor of {n} on the current device")
     return t.data_ptr()
 
@@ -398,16 +399,20 @@ def ds4sp_rope(x, rope: ds4sp_rope_config, out=None, positions=None, pos0: int =
     any token and head strides) and return ``out`` (of x's shape and type, allocated if None;
     x itself for in place). positions: int32 [n_tokens], or None for pos0 + i * pos_step.
     transpose: the transposed rotation, the gradient with respect to x."""
-    code = _rows(x, "x", 3)
+    dev = _device()
+    code = _rows(x, "x", 3, dev)
+    shape = x.shape
+    n, heads, head = shape
     if out is None:
-        out = x.new_empty(x.shape)
-    elif _rows(out, "out", 3) != code or out.shape != x.shape:
-        raise Ds4spError(ERR_INVALID_ARG, "out", f"expected {x.dtype} {tuple(x.shape)}")
-    n, heads, head = x.shape
-    xs, os_ = x.stride(), out.stride()
-    _check(load_library().ds4sp_rope(rope, x.data_ptr(), code, n, heads, head, xs[0], xs[1], out.data_ptr(),
-                                     os_[0], os_[1], _int_rows(positions, "positions", n), pos0, pos_step,
-                                     int(transpose), _stream(stream)), "ds4sp_rope")
+        out = x.new_empty(shape)
+    elif _rows(out, "out", 3, dev) != code or out.shape != shape:
+        raise Ds4spError(ERR_INVALID_ARG, "out", f"expected {x.dtype} {tuple(shape)}")
+    xt, xh, _ = x.stride()
+    ot, oh, _ = out.stride()
+    _check((_lib or load_library()).ds4sp_rope(
+        rope, x.data_ptr(), code, n, heads, head, xt, xh, out.data_ptr(), ot, oh,
+        _int_rows(positions, "positions", n, dev), pos0, pos_step, int(transpose), _stream_on(dev, stream)),
+        "ds4sp_rope")
     return out
 
 
@@ -422,9 +427,9 @@ def _cache_unit(kv_format: int, dims: int) -> Tuple[int, int]:
     return unit, ds4sp_cache_bytes(kv_format, dims, unit)
 
 
-def _cache(cache: torch.Tensor, kv_format: int, dims: int) -> int:
+def _cache(cache: torch.Tensor, kv_format: int, dims: int, dev: int) -> int:
     """Rows that a cache tensor (uint8, or float16 rows) holds in a format."""
-    if cache.get_device() != _device() or not cache.is_contiguous():
+    if cache.get_device() != dev or not cache.is_contiguous():
         raise Ds4spError(ERR_INVALID_ARG, "cache", "expected a contiguous tensor on the current CUDA device")
     if cache.dtype != torch.uint8 and not (kv_format == 0 and cache.dtype == torch.float16):
         raise Ds4spError(ERR_INVALID_ARG, "cache", f"dtype {cache.dtype}, expected uint8 (or float16 rows)")
@@ -439,30 +444,35 @@ def ds4sp_cache_write(cache, kv_format: int, x, row0: int, rope: Optional[ds4sp_
     """Store rows x [n, dims] (float16, bfloat16 or float32, any row stride) as rows row0 ..
     of ``cache`` (uint8, ds4sp_cache_bytes(kv_format, dims, rows) bytes; float16 rows for
     kv_format 0), after turning part of each (rope)."""
-    code = _rows(x, "x", 2)
+    dev = _device()
+    code = _rows(x, "x", 2, dev)
     n, dims = x.shape
-    rows = _cache(cache, kv_format, dims)
-    _check(load_library().ds4sp_cache_write(cache.data_ptr(), kv_format, dims, rows, row0, n, x.data_ptr(), code,
-                                            x.stride(0), rope, _int_rows(positions, "positions", n), pos0,
-                                            pos_step, _stream(stream)), "ds4sp_cache_write")
+    rows = _cache(cache, kv_format, dims, dev)
+    _check((_lib or load_library()).ds4sp_cache_write(
+        cache.data_ptr(), kv_format, dims, rows, row0, n, x.data_ptr(), code, x.stride(0), rope,
+        _int_rows(positions, "positions", n, dev), pos0, pos_step, _stream_on(dev, stream)), "ds4sp_cache_write")
 
 
 def ds4sp_cache_read(cache, kv_format: int, dims: int, rows=None, row0: int = 0, n: Optional[int] = None,
                      part: int = 0, out=None, dtype=torch.float16, stream=None):
     """Rows ``rows`` (int32) or row0 .. row0+n-1 of ``cache`` as values: returns ``out``
     ([n, dims], or [n, 512] for part 1, the value; allocated as ``dtype`` if None)."""
-    held = _cache(cache, kv_format, dims)
+    dev = _device()
+    held = _cache(cache, kv_format, dims, dev)
     if n is None:
         n = held - row0 if rows is None else rows.numel()
     width = 512 if part == 1 else dims
     if out is None:
-        out = torch.empty((max(n, 0), width), dtype=dtype, device=cache.device)
-    code = _rows(out, "out", 2)
-    if out.shape != (n, width):
-        raise Ds4spError(ERR_INVALID_ARG, "out", f"expected [{n}, {width}]")
-    _check(load_library().ds4sp_cache_read(cache.data_ptr(), kv_format, dims, held, _int_rows(rows, "rows", n),
-                                           row0, n, part, out.data_ptr(), code, out.stride(0), _stream(stream)),
-           "ds4sp_cache_read")
+        if dtype not in _DTYPES:
+            raise Ds4spError(ERR_INVALID_ARG, "dtype", f"{dtype}, expected float16, bfloat16 or float32")
+        out, code, stride = cache.new_empty((max(n, 0), width), dtype=dtype), _DTYPES[dtype], width
+    else:
+        code, stride = _rows(out, "out", 2, dev), out.stride(0)
+        if out.shape != (n, width):
+            raise Ds4spError(ERR_INVALID_ARG, "out", f"expected [{n}, {width}]")
+    _check((_lib or load_library()).ds4sp_cache_read(
+        cache.data_ptr(), kv_format, dims, held, _int_rows(rows, "rows", n, dev), row0, n, part, out.data_ptr(),
+        code, stride, _stream_on(dev, stream)), "ds4sp_cache_read")
     return out
 
 
