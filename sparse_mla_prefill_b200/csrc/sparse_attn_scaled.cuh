@@ -342,7 +342,9 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
 
     if (warp >= PWARP0 && warp < SMMA) {
         // ================================================================ gather
-        const int pw = warp - PWARP0, r = 32 * pw + lane;    // this thread resolves row r
+        // A warp copies rows 16 i + 4 pw + (0 .. 3), so that a short unit's rows are spread over the
+        // four; this thread resolves row r.
+        const int pw = warp - PWARP0, r = 16 * (lane >> 2) + 4 * pw + (lane & 3);
         const uint8_t* raw = reinterpret_cast<const uint8_t*>(p.kv_raw);
         const uint8_t* cmp = reinterpret_cast<const uint8_t*>(p.kv_cmp);
         // The top-k entry of a unit's row r, fetched a unit ahead.
@@ -365,19 +367,18 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
             if (ok && p.vis_mask) ok = p.vis_mask[(size_t)cu.it.t * p.mask_ld + j] != 0;
             return ok ? cmp + (size_t)e4m3_place(j) * DQK : raw + (size_t)e4m3_place(row) * DQK;
         };
-        // A warp copies 32 rows, four at a time: lane l takes chunk l % 8 of row l / 8 of the
-        // four, so an instruction covers four whole 128-byte lines.
-        const int ch = lane & 7, r4 = lane >> 3;
-        const uint32_t to_slab[2] = {(uint32_t)(32 * pw * 128 + r4 * 128 + ((ch ^ r4) << 4)),
-                                     (uint32_t)(32 * pw * 128 + r4 * 128 + ((ch ^ (r4 + 4)) << 4))};
-        const uint32_t to_rope = 32 * pw * 64 + r4 * 64;
+        // Four rows at a time: lane l takes chunk l % 8 of row l / 8 of the four, so an instruction
+        // covers four whole 128-byte lines.
+        const int ch = lane & 7, r4 = lane >> 3, r0 = 4 * pw + r4;
+        const uint32_t to_slab = r0 * 128 + ((ch ^ (r0 & 7)) << 4);
+        const uint32_t to_rope = r0 * 64 + ((ch ^ ((r0 >> 1) & 3)) << 4);
         int slot = 0, rope = 0;
         uint32_t slab_phase = 1, rope_phase = 1;
         int j = entry(c);
         while (c.valid) {
             bool ok;
             const uint8_t* mine = resolve(c, j, ok);
-            const bool copied = 32 * pw < c.rows();          // O^T reads whole groups of 32 rows
+            const int sixteens = (c.rows() + 31) / 32 * 2;   // O^T reads whole groups of 32 rows
             const int place = c.it.row0 + M * c.u + r;
             const int row = place < c.it.nsel ? j : c.it.s_lo + place - c.it.nsel;
             const uint8_t* scale = (place < c.it.nsel ? cmp : raw) + ((size_t)(row / kScaleBlock) * (kScaleBlock + 1) + kScaleBlock) * DQK;
@@ -393,11 +394,10 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     abort = true;                            // the whole warp gives up together
                     break;
                 }
-                if (copied) {
-                    const uint32_t dst = base + OFF_SLAB + slot * SLAB;
+                const uint32_t dst = base + OFF_SLAB + slot * SLAB + to_slab;
 #pragma unroll
-                    for (int it = 0; it < 8; ++it) cp_async_16(dst + to_slab[it & 1] + it * 512, src[it] + s * 128, true);
-                }
+                for (int it = 0; it < 8; ++it)
+                    if (it < sixteens) cp_async_16(dst + it * 2048, src[it] + s * 128, true);
                 cp_async_arrive_noinc(bar(B_SLAB_FULL + slot));
                 if (++slot == SLOTS) {
                     slot = 0;
@@ -405,11 +405,11 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 }
             }
             if (abort || !__all_sync(0xffffffffu, wait(B_ROPE_EMPTY + rope, rope_phase))) break;
-            if (copied && ch < 4) {
+            if (ch < 4) {
                 const uint32_t dst = base + OFF_ROPE + rope * ROPE + to_rope;
 #pragma unroll
                 for (int it = 0; it < 8; ++it)
-                    cp_async_16(dst + it * 256 + ((ch ^ ((2 * it + (r4 >> 1)) & 3)) << 4), src[it] + DV, true);
+                    if (it < sixteens) cp_async_16(dst + it * 1024, src[it] + DV, true);
             }
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + OFF_SCALE + (rope * M + r) * 4),
                          "l"(ok ? scale : raw), "r"(ok ? 4 : 0)
