@@ -27,8 +27,9 @@
 // is why the terms are columns.
 //
 // A slab of rows (128 rows x 128 bytes, the 128-byte swizzle) is the K-major A of S and, as
-// it lies, the MN-major A of O^T. Slabs form a ring of nine: O^T frees them one by one (its
-// tile m reads slab m only), and the gather of a later unit follows on its heels.
+// it lies, the MN-major A of O^T. There are slabs for two units: O^T frees them one by one (its
+// tile m reads slab m only), and the gather of the unit after next follows on its heels (nine
+// or ten slabs measured the same).
 //
 // Roles: warps 0-7 softmax, 8-11 the queries' terms and the output, 12-15 gather (16-byte
 // cp.async), warp 16 issues S and warp 17 O^T: an MMA of this size is short
@@ -53,8 +54,8 @@ constexpr int M = 128;                          // rows per unit
 constexpr int SPLIT_ROWS = attn::BR;            // rows of a unit in split mode
 constexpr int QT = 3;                           // terms of a query value
 constexpr int TILES = DV / 128;                 // value tiles = slabs of 128 dims
-constexpr int SLOTS = 9;                        // slab ring
-constexpr int ROPES = 3;                        // ring of the rows' last 64 dims
+constexpr int SLOTS = 2 * TILES;                // slabs: two units'
+constexpr int ROPES = 2;                        // the rows' last 64 dims, two units
 constexpr int SLAB = M * 128, ROPE = M * 64;
 constexpr int QROWS = QT * H;
 constexpr int QSLAB = QROWS * 128, QBYTES = TILES * QSLAB + QROWS * 64;
@@ -372,10 +373,10 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
         const int ch = lane & 7, r4 = lane >> 3, r0 = 4 * pw + r4;
         const uint32_t to_slab = r0 * 128 + ((ch ^ (r0 & 7)) << 4);
         const uint32_t to_rope = r0 * 64 + ((ch ^ ((r0 >> 1) & 3)) << 4);
-        int slot = 0, rope = 0;
-        uint32_t slab_phase = 1, rope_phase = 1;
         int j = entry(c);
-        while (c.valid) {
+        for (int g = 0; c.valid; ++g) {
+            const int b = g & 1;
+            const uint32_t phase = ((g >> 1) & 1) ^ 1;
             bool ok;
             const uint8_t* mine = resolve(c, j, ok);
             const int sixteens = (c.rows() + 31) / 32 * 2;   // O^T reads whole groups of 32 rows
@@ -390,35 +391,27 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
             j = entry(c);
 #pragma unroll
             for (int s = 0; s < TILES; ++s) {
-                if (!__all_sync(0xffffffffu, wait(B_SLAB_EMPTY + slot, slab_phase))) {
+                if (!__all_sync(0xffffffffu, wait(B_SLAB_EMPTY + b * TILES + s, phase))) {
                     abort = true;                            // the whole warp gives up together
                     break;
                 }
-                const uint32_t dst = base + OFF_SLAB + slot * SLAB + to_slab;
+                const uint32_t dst = base + OFF_SLAB + (b * TILES + s) * SLAB + to_slab;
 #pragma unroll
                 for (int it = 0; it < 8; ++it)
                     if (it < sixteens) cp_async_16(dst + it * 2048, src[it] + s * 128, true);
-                cp_async_arrive_noinc(bar(B_SLAB_FULL + slot));
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    slab_phase ^= 1;
-                }
+                cp_async_arrive_noinc(bar(B_SLAB_FULL + b * TILES + s));
             }
-            if (abort || !__all_sync(0xffffffffu, wait(B_ROPE_EMPTY + rope, rope_phase))) break;
+            if (abort || !__all_sync(0xffffffffu, wait(B_ROPE_EMPTY + b, phase))) break;
             if (ch < 4) {
-                const uint32_t dst = base + OFF_ROPE + rope * ROPE + to_rope;
+                const uint32_t dst = base + OFF_ROPE + b * ROPE + to_rope;
 #pragma unroll
                 for (int it = 0; it < 8; ++it)
                     if (it < sixteens) cp_async_16(dst + it * 1024, src[it] + DV, true);
             }
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + OFF_SCALE + (rope * M + r) * 4),
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + OFF_SCALE + (b * M + r) * 4),
                          "l"(ok ? scale : raw), "r"(ok ? 4 : 0)
                          : "memory");
-            cp_async_arrive_noinc(bar(B_ROPE_FULL + rope));
-            if (++rope == ROPES) {
-                rope = 0;
-                rope_phase ^= 1;
-            }
+            cp_async_arrive_noinc(bar(B_ROPE_FULL + b));
         }
         if (p.prefetch_bytes > 0 && !abort) {
             // This CTA's slice of the region the next kernel reads, in pieces of up to 32 KB.
@@ -437,37 +430,28 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
             return !abort;
         };
         if (warp == SMMA) {                                  // S of each unit
-            int slot = 0, rope = 0;
-            uint32_t slab_phase = 0, rope_phase = 0;
             for (int g = 0; c.valid && !abort; ++g, c.advance(p, items)) {
+                const int b = g & 1;
+                const uint32_t phase = (g >> 1) & 1;
                 if (c.u == 0 && !wait_w(B_Q_FULL, c.m & 1)) break;
-                if (!wait_w(B_S_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1)) break;
+                if (!wait_w(B_S_EMPTY + b, phase ^ 1)) break;
                 tc_fence_after();
-                const uint32_t d = tmem + TM_S + (g & 1) * QROWS;
+                const uint32_t d = tmem + TM_S + b * QROWS;
 #pragma unroll 1
                 for (int s = 0; s < TILES; ++s) {
-                    if (!wait_w(B_SLAB_FULL + slot, slab_phase)) break;
+                    if (!wait_w(B_SLAB_FULL + b * TILES + s, phase)) break;
                     fence_async_proxy();
-                    umma_e4m3<DESC_128, DESC_128, 32, 32>(d, base + OFF_SLAB + slot * SLAB, base + OFF_Q + s * QSLAB,
+                    umma_e4m3<DESC_128, DESC_128, 32, 32>(d, base + OFF_SLAB + (b * TILES + s) * SLAB, base + OFF_Q + s * QSLAB,
                                                           idesc(QROWS, false), s, 4);
-                    if (++slot == SLOTS) {
-                        slot = 0;
-                        slab_phase ^= 1;
-                    }
                 }
-                if (abort || !wait_w(B_ROPE_FULL + rope, rope_phase)) break;
+                if (abort || !wait_w(B_ROPE_FULL + b, phase)) break;
                 fence_async_proxy();
-                umma_e4m3<DESC_64, DESC_64, 32, 32>(d, base + OFF_ROPE + rope * ROPE, base + OFF_Q + TILES * QSLAB,
+                umma_e4m3<DESC_64, DESC_64, 32, 32>(d, base + OFF_ROPE + b * ROPE, base + OFF_Q + TILES * QSLAB,
                                                     idesc(QROWS, false), 1, 2);
-                commit_elected(bar(B_S_FULL + (g & 1)));
+                commit_elected(bar(B_S_FULL + b));
                 if (c.last()) commit_elected(bar(B_Q_EMPTY));
-                if (++rope == ROPES) {
-                    rope = 0;
-                    rope_phase ^= 1;
-                }
             }
         } else {                                             // O^T
-            int slot = 0;
             for (int g = 0; c.valid && !abort; ++g, c.advance(p, items)) {
                 const int b = g & 1, steps = (c.rows() + 31) / 32;
                 const bool first = c.u == 0;
@@ -478,10 +462,9 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     // (a token's first unit overwrites tile by tile, behind the output's reads)
                     if (first && !wait_w(B_O_EMPTY + t, (c.m & 1) ^ 1)) break;
                     tc_fence_after();
-                    umma_e4m3<DESC_128, DESC_P, 32 * 128, 32 * H>(d + t * OC, base + OFF_SLAB + slot * SLAB,
+                    umma_e4m3<DESC_128, DESC_P, 32 * 128, 32 * H>(d + t * OC, base + OFF_SLAB + (b * TILES + t) * SLAB,
                                                                   base + OFF_P + b * PBUF, idesc(OC, true), !first, steps);
-                    commit_elected(bar(B_SLAB_EMPTY + slot));
-                    if (++slot == SLOTS) slot = 0;
+                    commit_elected(bar(B_SLAB_EMPTY + b * TILES + t));
                 }
                 if (abort) break;
                 commit_elected(bar(B_P_EMPTY + b));
@@ -500,7 +483,6 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
         const float* qs = reinterpret_cast<const float*>(smem + OFF_QS) + hg * HG;
         const int group_bar = SOFTMAX_BAR + hg;
         F2 nref[HG / 2], sum[HG / 2], cq[HG / 2];            // minus the references, sums, logit factors
-        int rope = 0;
         for (int g = 0; c.valid; ++g, c.advance(p, items)) {
             const bool first = c.u == 0;
             wait(B_P_EMPTY + (g & 1), ((g >> 1) & 1) ^ 1);   // O^T of the unit before last: its weights
@@ -508,7 +490,7 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
             __syncwarp();
             tc_fence_after();
             // (S was issued after its issuer saw the unit's rows, and scales, arrive.)
-            const float sv = scales[rope * M + r];
+            const float sv = scales[(g & 1) * M + r];
             const bool valid = sv > 0.f;
             const int sexp = (int)(__float_as_uint(sv) >> 23) - 127;
             if (first) {
@@ -544,9 +526,8 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar(B_S_EMPTY + (g & 1)));
-                mbar_arrive(bar(B_ROPE_EMPTY + rope));
+                mbar_arrive(bar(B_ROPE_EMPTY + (g & 1)));
             }
-            if (++rope == ROPES) rope = 0;
             float w[HG];                                     // x - ref, then the weights
             float top = -INFINITY;
             auto against_ref = [&] {
