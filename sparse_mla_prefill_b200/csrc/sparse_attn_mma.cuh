@@ -616,6 +616,9 @@ __global__ void __launch_bounds__(attn::Roles<KVF>::THREADS, 1) sparse_attn_mma_
                 for (long long off = lo + (long long)pw * 32768; off < hi; off += R::PW * 32768LL)
                     prefetch_l2(p.prefetch + off, (uint32_t)min(32768LL, hi - off));
         }
+        // Copies into shared memory end before the CTA does. Fp16 rows are in no group yet, and
+        // after a give-up no consumer has waited for them.
+        cp_async_commit();
         cp_async_wait<0>();
     } else {
         // ================================================================ consumers

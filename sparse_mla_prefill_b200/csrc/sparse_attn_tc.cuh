@@ -183,6 +183,9 @@ __global__ void __launch_bounds__(tcattn::THREADS, 1) sparse_attn_tc_kernel(Attn
                 cp_async_arrive_noinc(t_full);
             }
         }
+        // Copies into shared memory end before the CTA does (the rows are in no group yet, and
+        // after a give-up nobody has waited for them).
+        cp_async_commit();
         cp_async_wait<0>();
     } else if (warp == MWARP) {
         // ================================================================ MMA issuer
