@@ -21,10 +21,19 @@
 // e4m3 is of what the terms before it left, so nothing is lost but the last one's remainder.
 // Products of e4m3 values are exact in the fp32 accumulator.
 //
-// What bounds it: each unit's rows pass through the tensor cores twice, from shared memory.
-// An M = 128, K = 32 instruction takes about 50 cycles whatever N up to 80 (measured: its
-// 4 KB of A), so 128 rows take 18 + 16 of them, about 1,750 cycles. N costs nothing, which
-// is why the terms are columns.
+// What bounds it: shared memory, and the instructions around it. Each unit's rows pass through
+// the tensor cores twice, from shared memory: an M = 128, K = 32 instruction takes what its
+// operands take at 128 bytes a cycle (measured: 45 cycles for S, 53 for O^T, mostly the 4 KB of
+// A), so 128 rows take 18 + 16 of them, about 1,640 cycles, and N costs little, which is why the
+// terms are columns. The gather and the roles' own accesses add about 800. Measured, 10,240
+// tokens with 512 + 128 rows each: 565 us (pv_mode 1; each SM 3,300 cycles a unit; the softmax
+// is busy for 2,500 of them, the tensor pipe for half, shared memory for 75%), against 1,097 us
+// of the fp16 cache's kernel with fp16 probabilities, 1,290 us with fp32-staged ones.
+//
+// What did not help: gathers by TMA (26 cycles for each 512 bytes), two groups of gather warps,
+// more slabs, queries in warps of their own or double-buffered, a vote whose wait runs under the
+// weights, sleeping or busier waits. The roles' loops compete for the instruction caches, so
+// code size counts.
 //
 // A slab of rows (128 rows x 128 bytes, the 128-byte swizzle) is the K-major A of S and, as
 // it lies, the MN-major A of O^T. There are slabs for two units: O^T frees them one by one (its
@@ -784,34 +793,34 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
 #pragma unroll 1
             for (int t = 0; t < TILES; ++t) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int h0 = half * HG;
-                uint32_t o[NT][8];
+                for (int half = 0; half < 2; ++half) {
+                    const int h0 = half * HG;
+                    uint32_t o[NT][8];
 #pragma unroll
-                for (int k = 0; k < NT; ++k) tmem_ld_x8(tmem + lanes + TM_O + t * OC + o_col<NT>(half, k), o[k]);
-                tmem_ld_wait();
+                    for (int k = 0; k < NT; ++k) tmem_ld_x8(tmem + lanes + TM_O + t * OC + o_col<NT>(half, k), o[k]);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < NT; ++k) regs_after_wait(o[k]);
-                if (half == 1) {                             // the tile is read (and the sums)
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(B_O_EMPTY + t));
-                        if (t + 1 == TILES) mbar_arrive(bar(B_L_EMPTY + (m & 1)));
+                    for (int k = 0; k < NT; ++k) regs_after_wait(o[k]);
+                    if (half == 1) {                             // the tile is read (and the sums)
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(B_O_EMPTY + t));
+                            if (t + 1 == TILES) mbar_arrive(bar(B_L_EMPTY + (m & 1)));
+                        }
+                    }
+                    float* to = out + h0 * DV + 128 * t + 32 * ew + lane;
+#pragma unroll
+                    for (int h = 0; h < HG; h += 2) {
+                        auto two = [&](int k) { return f2(__uint_as_float(o[k][h]), __uint_as_float(o[k][h + 1])); };
+                        F2 v = two(NT - 1);
+#pragma unroll
+                        for (int k = NT - 2; k >= 0; --k) v = fma2(v, f2(1.f / term_step(k), 1.f / term_step(k)), two(k));
+                        const float2 f = of_f2(mul2(v, by[(h0 + h) / 2]));
+                        to[h * DV] = f.x;
+                        to[(h + 1) * DV] = f.y;
                     }
                 }
-                float* to = out + h0 * DV + 128 * t + 32 * ew + lane;
-#pragma unroll
-                for (int h = 0; h < HG; h += 2) {
-                    auto two = [&](int k) { return f2(__uint_as_float(o[k][h]), __uint_as_float(o[k][h + 1])); };
-                    F2 v = two(NT - 1);
-#pragma unroll
-                    for (int k = NT - 2; k >= 0; --k) v = fma2(v, f2(1.f / term_step(k), 1.f / term_step(k)), two(k));
-                    const float2 f = of_f2(mul2(v, by[(h0 + h) / 2]));
-                    to[h * DV] = f.x;
-                    to[(h + 1) * DV] = f.y;
-                }
-              }
             }
         }
     }
