@@ -14,7 +14,10 @@
 //
 // Bound: memory (each value read and written once). A thread keeps one chunk of the head and
 // walks rows (token, head), four loads in flight; the block computes its tokens' cos and sin
-// once, into shared memory, for all heads, while its first loads are on their way.
+// once, into shared memory, for all heads, while its first loads are on their way. Measured:
+// 10,240 tokens x 64 heads of 128 bf16 values (336 MB) in 52.4 us, the copy rate; 10,240 x 16
+// heads of 64 fp16 values from rows of 192 into rows of 576 (42 MB in 128-byte pieces) in 10.5 us.
+// With a thread per chunk that computed its own cos and sin the first took 150 us.
 #pragma once
 
 #include <cuda_bf16.h>
