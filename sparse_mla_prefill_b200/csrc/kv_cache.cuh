@@ -332,11 +332,12 @@ __device__ __forceinline__ uint2 codes_of(const Eight<T>& a, unsigned long long 
 // eighth chunk of eight values. HELD (up to 576 dims, aligned): the unrotated values as they
 // were loaded stay in registers between the block's maximum and the rounding, all loads in
 // flight at once (16-bit values: 64 registers, two CTAs an SM, so that one block's loads run
-// under the other's arithmetic). What is not held, the rotated chunks among it, is a loop of
-// its own and computed twice. Measured, 122,880 bf16
-// rows of 576 with 64 rotary dims: 213 MB in 52.5 us (4.1 TB/s, 0.63 of the copy rate), bound by
-// instruction issue and by the blocks' two phases (each value is unpacked, scaled and converted
-// in fp32).
+// under the other's arithmetic), and of a rotated part of up to 64 dims the one chunk that a
+// lane has, turned once. What is not held is a loop of its own and computed twice (a rotated
+// part of 64 dims that way: 52.6 us below). Measured, 122,880 bf16 rows of 576 with 64 rotary
+// dims: 213 MB in 47.4 us (4.5 TB/s, 0.70 of the copy rate), bound by the blocks' two phases and
+// by instruction issue (each value is unpacked, scaled and converted in fp32). A CTA that goes
+// on to another block, loading it as it stores this one's chunks, spills: 78 us.
 template <class T, bool HELD>
 __global__ void __launch_bounds__(kE4M3Threads, sizeof(T) == 2 ? 2 : 1)
 cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab,
@@ -351,9 +352,12 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
     uint8_t* base = cache + (long long)blk * (kScaleBlock + 1) * p.dims;
     float* record = reinterpret_cast<float*>(base + kScaleBlock * p.dims);
     const int old = blockIdx.x == 0 ? p.row0 % kScaleBlock : 0;   // rows kept from before
-    // HELD: the chunks of steps in `held` are in registers; rotated ones are [rot0, rot1).
+    // HELD: the chunks of steps in `held` are in registers; rotated ones are [rot0, rot1), at most
+    // one a lane where `one`: it is turned once, while the others' loads are on their way.
     const int rot0 = p.rotate ? tab.offset / 8 : 0, rot1 = p.rotate ? rot0 + tab.dims / 8 : 0;
-    Eight<T> v[HELD ? kE4M3Held : 1];
+    const bool one = HELD && rot1 - rot0 <= 8, mine = one && in && l < rot1 - rot0;
+    const int loop0 = HELD ? rot0 : 0, loop1 = HELD ? (one ? rot0 : rot1) : chunks;
+    Eight<T> v[HELD ? kE4M3Held : 1], turn;
     uint32_t held = 0;
     if constexpr (HELD)
         if (in) {
@@ -366,15 +370,21 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
                     v[s] = load_eight(row + 64 * s);
                 }
             }
+            if (mine) turn = load_eight(row + 8 * rot0);
         }
     const float old_scale = old ? *record : 0.f;
     load_steps(tab, p.rotate, step);
 
-    float top = 0.f;
+    float top = 0.f, turned_to[8];
+    if constexpr (HELD)
+        if (mine) {
+            turn_eight<T>(p, tab, step, i, rot0 + l, turn, turned_to);
+            top = top_of(turned_to, top);
+        }
     if (in) {
         // (without HELD every chunk goes this way)
 #pragma unroll 1
-        for (int c = (HELD ? rot0 : 0) + l; c < (HELD ? rot1 : chunks); c += 8) {
+        for (int c = loop0 + l; c < loop1; c += 8) {
             float u[8];
             load_chunk<T>(p, tab, step, i, c, u);
             top = top_of(u, top);
@@ -430,8 +440,10 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
 #pragma unroll
         for (int s = 0; s < kE4M3Held; ++s)
             if (held >> s & 1u) *reinterpret_cast<uint2*>(to + 64 * s) = codes_of<T>(v[s], inv2);
+    if constexpr (HELD)
+        if (mine) *reinterpret_cast<uint2*>(to + 8 * rot0) = codes_of(turned_to, inv2);
 #pragma unroll 1
-    for (int c = (HELD ? rot0 : 0) + l; c < (HELD ? rot1 : chunks); c += 8) {
+    for (int c = loop0 + l; c < loop1; c += 8) {
         float u[8];
         load_chunk<T>(p, tab, step, i, c, u);
         *reinterpret_cast<uint2*>(base + (long long)r * p.dims + 8 * c) = codes_of(u, inv2);
