@@ -274,32 +274,26 @@ __device__ __forceinline__ float top_of(const Eight<T>& a, float top) {
     return top_of(u, top);
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Magnitudes as integers: without its sign a float orders as its bits do. The larger of `bits`
-// (one 32-bit value, or two 16-bit ones) and a chunk's, infinities and NaNs included.
+// The larger of `top` (a value, or two) and a chunk's magnitudes: infinities included, NaNs not.
+__device__ __forceinline__ float larger(float top, float v) { return fmaxf(top, fabsf(v)); }
+__device__ __forceinline__ __half2 larger(__half2 top, __half2 v) { return __hmax2(top, __habs2(v)); }
+__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 top, __nv_bfloat162 v) { return __hmax2(top, __habs2(v)); }
+template <class T> struct Packed { using type = __half2; };
+template <> struct Packed<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <> struct Packed<float> { using type = float; };
 template <class T>
-__device__ __forceinline__ uint32_t top_bits(const Eight<T>& a, uint32_t bits) {
+__device__ __forceinline__ typename Packed<T>::type top_packed(const Eight<T>& a, typename Packed<T>::type top) {
 #pragma unroll
     for (int w = 0; w < (int)sizeof(T) / 2; ++w) {
         const uint32_t u[4] = {a.q[w].x, a.q[w].y, a.q[w].z, a.q[w].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            bits = sizeof(T) == 4 ? max(bits, u[k] & 0x7fffffffu) : max_u16x2(bits, u[k] & 0x7fff7fffu);
+        for (int k = 0; k < 4; ++k) top = larger(top, *reinterpret_cast<const typename Packed<T>::type*>(&u[k]));
     }
-    return bits;
+    return top;
 }
-__device__ __forceinline__ float top_value(uint32_t bits, float) { return __uint_as_float(bits); }
-__device__ __forceinline__ float top_value(uint32_t bits, __half) {
-    return __half2float(__ushort_as_half((unsigned short)max(bits & 0xffffu, bits >> 16)));
-}
-__device__ __forceinline__ float top_value(uint32_t bits, __nv_bfloat16) {
-    return __uint_as_float(max(bits & 0xffffu, bits >> 16) << 16);
-}
+__device__ __forceinline__ float top_value(float top) { return top; }
+__device__ __forceinline__ float top_value(__half2 top) { return fmaxf(__low2float(top), __high2float(top)); }
+__device__ __forceinline__ float top_value(__nv_bfloat162 top) { return fmaxf(__low2float(top), __high2float(top)); }
 
 // Eight values times 2^-e (inv, twice) as codes.
 __device__ __forceinline__ uint2 codes_of(const float (&u)[8], unsigned long long inv2) {
@@ -343,7 +337,7 @@ __global__ void __launch_bounds__(kE4M3Threads, sizeof(T) == 2 ? 2 : 1)
 cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab,
                         uint8_t* __restrict__ cache) {
     __shared__ uint64_t step[kRopeMaxDims / 2];
-    __shared__ float warp_top[kE4M3Threads / 32];
+    __shared__ uint32_t warp_top[kE4M3Threads / 32];
     const int tid = threadIdx.x, r = tid / 8, l = tid % 8;
     const int blk = p.row0 / kScaleBlock + blockIdx.x;
     const int i = (int)((long long)blk * kScaleBlock + r - p.row0);      // this lane's row of the written ones
@@ -390,26 +384,27 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
             top = top_of(u, top);
         }
         if constexpr (HELD) {
-            uint32_t bits = 0u;
+            using Two = typename Packed<T>::type;
+            Two two;
+            memset(&two, 0, sizeof(two));
 #pragma unroll
             for (int s = 0; s < kE4M3Held; ++s)
-                if (held >> s & 1u) bits = top_bits<T>(v[s], bits);
-            const float t = top_value(bits, T{});
+                if (held >> s & 1u) two = top_packed<T>(v[s], two);
+            const float t = top_value(two);
             if (t <= 3.402823466e38f) {
                 top = fmaxf(top, t);
-            } else {                                      // an infinity or a NaN: the finite ones
+            } else {                                      // an infinity: the finite ones
 #pragma unroll
                 for (int s = 0; s < kE4M3Held; ++s)
                     if (held >> s & 1u) top = top_of<T>(v[s], top);
             }
         }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (tid % 32 == 0) warp_top[tid / 32] = top;
+    // (a float that is not negative orders as its bits do)
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if (tid % 32 == 0) warp_top[tid / 32] = most;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kE4M3Threads / 32; ++w) top = fmaxf(top, warp_top[w]);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, warp_top[tid % (kE4M3Threads / 32)]));
     int e = scale_exponent(top);
     if (old) {
         const int was = (int)(__float_as_uint(old_scale) >> 23) - 127;
