@@ -328,10 +328,11 @@ __device__ __forceinline__ uint2 codes_of(const Eight<T>& a, unsigned long long 
 // flight at once (16-bit values: 64 registers, two CTAs an SM, so that one block's loads run
 // under the other's arithmetic), and of a rotated part of up to 64 dims the one chunk that a
 // lane has, turned once. What is not held is a loop of its own and computed twice (a rotated
-// part of 64 dims that way: 52.6 us below). Measured, 122,880 bf16 rows of 576 with 64 rotary
-// dims: 213 MB in 47.4 us (4.5 TB/s, 0.70 of the copy rate), bound by the blocks' two phases and
-// by instruction issue (each value is unpacked, scaled and converted in fp32). A CTA that goes
-// on to another block, loading it as it stores this one's chunks, spills: 78 us.
+// part of 64 dims that way: 5 us more below). Measured, 122,880 bf16 rows of 576 with 64 rotary
+// dims: 213 MB in 46.0 us (4.6 TB/s, 0.72 of the copy rate), bound by the blocks' two phases and
+// by instructions (issue 59% busy, the integer pipe 55%: each value is unpacked, scaled and
+// converted in fp32). A CTA that goes on to another block, loading it as it stores this one's
+// chunks, spills: 78 us; the next block prefetched to L2: the same time.
 template <class T, bool HELD>
 __global__ void __launch_bounds__(kE4M3Threads, sizeof(T) == 2 ? 2 : 1)
 cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab,
