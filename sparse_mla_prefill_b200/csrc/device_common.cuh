@@ -104,6 +104,14 @@ __device__ __forceinline__ void give_up(const WaitCtl& w) {
     if (w.abort_word) *reinterpret_cast<volatile uint32_t*>(w.abort_word) = w.epoch;
 }
 
+// What a role that gave up does last, before its CTA ends: arrivals of copies and of commits
+// have no wait of their own where nobody waits for their phase any more, so the CTA, whose
+// shared memory they write, stays for 50 us (bounded by the clock alone).
+__device__ __forceinline__ void linger() {
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 50000ull) __nanosleep(1000);
+}
+
 // Wait for the phase of the given parity to complete. Gives up (returns false, records
 // kStatusTimeout and sets `abort`) once w.limit_ns has passed since the first miss, or
 // as soon as another wait of the same launch has given up. Once `abort` is set it

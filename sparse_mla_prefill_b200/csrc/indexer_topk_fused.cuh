@@ -408,6 +408,7 @@ indexer_topk_fused_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
     }
 
+    if (abort) linger();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

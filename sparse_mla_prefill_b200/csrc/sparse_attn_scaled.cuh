@@ -825,7 +825,10 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
         }
     }
 
-    if (abort) give_up(p.wc);
+    if (abort) {
+        give_up(p.wc);
+        linger();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
