@@ -281,7 +281,9 @@ ds4sp_status ds4sp_debug_fail_launches(ds4sp_handle* h, int n);
  * whatever is set here (they complete on their own). A give-up in one launch does not
  * shorten the waits of later launches.
  *   ns  the limit for this handle's later launches, in nanoseconds; 0 = give up at the
- *       first wait that is not already complete; negative = back to the default. */
+ *       first wait that is not already complete; negative = back to the default.
+ * Below the default the indexer and the top-k run as two kernels whatever topk_mode says:
+ * the fused kernel's give-up is not provoked. */
 ds4sp_status ds4sp_debug_set_wait_limit_ns(ds4sp_handle* h, long long ns);
 
 /* Explicit-mask visibility, a debug form of the path for the "explicit-mask versus

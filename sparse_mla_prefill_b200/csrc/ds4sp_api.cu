@@ -493,7 +493,9 @@ ds4sp_status dispatch_indexer_h(ds4sp_handle* h, const void* q_idx, const void* 
 // Indexer and top-k in one launch (indexer_topk_fused_kernel), when the call qualifies:
 // no explicit mask, some token sees a compressed row, the key rows of a token block fit
 // one of the kernel's two 40 KB key buffers (2,560 rows, a 10,240-token context, at 64
-// index heads) and the launch has at most kFusedMaxBlocks token blocks.
+// index heads), the launch has at most kFusedMaxBlocks token blocks, and the wait limit is
+// not lowered: at the limit 0 about one prefill in four by this kernel ended in a launch
+// failure, whose cause reading has not shown, so its give-up is not provoked.
 // Returns DS4SP_ERR_UNSUPPORTED (with nothing launched) when it does not qualify.
 template <int D_I, int H_I>
 ds4sp_status launch_fused(ds4sp_handle* h, const void* q_idx, const void* k_idx, const float* w,
@@ -505,7 +507,7 @@ ds4sp_status launch_fused(ds4sp_handle* h, const void* q_idx, const void* k_idx,
     const int max_tiles = (n_rows + C::BM - 1) / C::BM;
     const int kld = C::BM * max_tiles;
     if (h->mask || n_rows == 0 || n_tb > kFusedMaxBlocks ||
-        (long long)C::TB * kld * 4 > C::KEY_BYTES)
+        (long long)C::TB * kld * 4 > C::KEY_BYTES || h->wait_limit_ns < kWaitLimitNs)
         return DS4SP_ERR_UNSUPPORTED;
     CUtensorMap tk, tq;
     if (!make_tmap_2d(&tk, k_idx, D_I, n_rows, C::BM) ||
