@@ -74,6 +74,7 @@ constexpr int EWARP0 = SWARPS, PWARP0 = EWARP0 + EWARPS, SMMA = PWARP0 + PWARPS,
 constexpr int THREADS = (OMMA + 1) * 32;
 constexpr int SOFTMAX_BAR = 1;                  // and 2: one per group
 constexpr int OUT_BAR = 3;
+constexpr float UNSET = 1e30f;                  // minus the reference while no row was attended
 constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference, which is
 constexpr float start_of(int nt) { return nt == 5 ? 5.f : 3.f; }   // set so many above a unit's maximum
 
@@ -510,9 +511,13 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     cq[2 * q] = f2(f.x, f.y);
                     cq[2 * q + 1] = f2(f.z, f.w);
                 }
+            }
+            // No row of the item attended before this unit: the units before it, if there are
+            // any, were all hidden and left sums and O of zero.
+            const bool none = first || of_f2(nref[0]).x == UNSET;
+            if (none)
 #pragma unroll
                 for (int q = 0; q < HG / 2; ++q) nref[q] = sum[q] = f2(0.f, 0.f);
-            }
             F2 x[HG / 2];                                    // log2 of the row's weights
             {
                 uint32_t d0[8], d1[8], d2[8];
@@ -549,8 +554,8 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 }
             };
             against_ref();
-            if (first || named_barrier_or(group_bar, 128, abort || (valid && top > HEADROOM))) {
-                // A new reference: the first unit's maximum, or one raised by this unit.
+            if (none || named_barrier_or(group_bar, 128, abort || (valid && top > HEADROOM))) {
+                // A new reference: the first rows' maximum, or one raised by this unit.
                 float* red = reinterpret_cast<float*>(smem + OFF_RED) + ((g & 1) * H + hg * HG) * 4;   // [head][quarter]
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
@@ -558,22 +563,23 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     if (lane == 0) red[4 * h + qd] = mx;
                 }
                 if (named_barrier_or(group_bar, 128, abort)) break;
-                float alpha[HG];
+                float alpha[HG], most = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
                     const float4 m4 = *reinterpret_cast<const float4*>(red + 4 * h);
                     const float mu = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                    const float up = (first ? mu > -INFINITY : mu > HEADROOM) ? mu + start_of(NT) : 0.f;
+                    const float up = (none ? mu > -INFINITY : mu > HEADROOM) ? mu + start_of(NT) : 0.f;
+                    most = fmaxf(most, mu);
                     alpha[h] = fast_exp2(-up);
                     w[h] = -up;
                 }
 #pragma unroll
                 for (int q = 0; q < HG / 2; ++q) {
                     nref[q] = add2(nref[q], f2(w[2 * q], w[2 * q + 1]));
-                    if (!first) sum[q] = mul2(sum[q], f2(alpha[2 * q], alpha[2 * q + 1]));
+                    if (!none) sum[q] = mul2(sum[q], f2(alpha[2 * q], alpha[2 * q + 1]));
                 }
                 against_ref();
-                if (!first) {
+                if (!none) {
                     // O^T of the units before has run; this one's waits for the weights below.
                     wait(B_P_EMPTY + ((g - 1) & 1), ((g - 1) >> 1) & 1);
                     __syncwarp();
@@ -595,6 +601,9 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                     }
                     tmem_st_wait();
                 }
+                if (most == -INFINITY)                       // (the same in the whole group)
+#pragma unroll
+                    for (int q = 0; q < HG / 2; ++q) nref[q] = f2(UNSET, UNSET);
             }
             // Weights, their share of the sums, and their terms: w = hi + lo, two fp16 values;
             // two terms of hi, and NT - 2 of what they leave, lo joining it (NT = 5).
