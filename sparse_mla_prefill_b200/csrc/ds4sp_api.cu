@@ -965,7 +965,7 @@ ds4sp_status make_rope_table(const ds4sp_rope_config* cfg, RopeTable* tab) {
         tab->step[i] = ((uint64_t)top << 32) + (uint64_t)std::ldexp(std::ldexp(frac, 32) - top, 32);
     }
     const double m = c.mscale > 0.0 ? c.mscale : c.scaling == 3 && s > 1.0 ? 0.1 * std::log(s) + 1.0 : 1.0;
-    tab->m = (float)m;
+    tab->m = m;
     tab->dims = c.dims;
     tab->offset = c.offset;
     tab->half_layout = c.layout;
@@ -1016,16 +1016,24 @@ template <class T>
 void launch_cache_write_t(const CacheRows& p, const RopeTable& tab, uint8_t* cache, int fmt, int rb, cudaStream_t s) {
     const unsigned grid = (unsigned)(((long long)p.n * (p.dims / 8) + 255) / 256);
     const unsigned blocks = (unsigned)((p.row0 % kScaleBlock + (long long)p.n + kScaleBlock - 1) / kScaleBlock);
+    auto plain = [&](auto turned, auto not_turned) {
+        if (p.rotate) turned<<<grid, 256, 0, s>>>(p, tab, cache, rb);
+        else not_turned<<<grid, 256, 0, s>>>(p, tab, cache, rb);
+    };
     switch (fmt) {
-        case kFmtF16: cache_write_kernel<T, kFmtF16><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
-        case kFmtQ8: cache_write_kernel<T, kFmtQ8><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
-        case kFmtQ4: cache_write_kernel<T, kFmtQ4><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
-        case kFmtQ8Q4: cache_write_kernel<T, kFmtQ8Q4><<<grid, 256, 0, s>>>(p, tab, cache, rb); break;
+        case kFmtF16: plain(cache_write_kernel<T, kFmtF16, true>, cache_write_kernel<T, kFmtF16, false>); break;
+        case kFmtQ8: plain(cache_write_kernel<T, kFmtQ8, true>, cache_write_kernel<T, kFmtQ8, false>); break;
+        case kFmtQ4: plain(cache_write_kernel<T, kFmtQ4, true>, cache_write_kernel<T, kFmtQ4, false>); break;
+        case kFmtQ8Q4: plain(cache_write_kernel<T, kFmtQ8Q4, true>, cache_write_kernel<T, kFmtQ8Q4, false>); break;
         default:
-            if (p.dims <= 64 * kE4M3Held && p.fast)
-                cache_write_e4m3_kernel<T, true><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
+            if (p.dims > 64 * kE4M3Held || !p.fast)
+                cache_write_e4m3_kernel<T, false, kTurnedTwice><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
+            else if (!p.rotate)
+                cache_write_e4m3_kernel<T, true, kNotTurned><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
+            else if (tab.dims <= 64)
+                cache_write_e4m3_kernel<T, true, kTurnedOnce><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
             else
-                cache_write_e4m3_kernel<T, false><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
+                cache_write_e4m3_kernel<T, true, kTurnedTwice><<<blocks, kE4M3Threads, 0, s>>>(p, tab, cache);
     }
 }
 

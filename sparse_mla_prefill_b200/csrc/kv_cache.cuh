@@ -1,7 +1,7 @@
 // Writing latent rows to a cache as they are produced, and reading them back.
 //
 // A row of x (fp16, bf16 or fp32) is rotated (optionally, the rotary part of the row:
-// rope.cuh's arithmetic, kept in fp32) and stored in the cache's format: fp16, the block
+// rope.cuh's arithmetic, kept in fp32, or in 64 bits for kv_format 5) and stored in the cache's format: fp16, the block
 // formats of quant_kv.cuh, or kv_format 5, whose rows the scaled attention reads:
 //
 //   e4m3 codes with one scale 2^e for each block of 64 rows; value = code * 2^e.
@@ -21,6 +21,8 @@
 #pragma once
 
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "quant_kv.cuh"
 #include "rope.cuh"
@@ -79,60 +81,89 @@ __device__ __forceinline__ bool turned(const CacheRows& p, const RopeTable& tab,
     return p.rotate && 8 * c >= tab.offset && 8 * c < tab.offset + tab.dims;
 }
 
+// A 64-bit value cut to fp32, the last bit set where anything was cut off, so that a later
+// rounding to fewer bits is the rounding of the 64-bit value. (Turned in fp32, or rounded to it
+// in between, one value in some millions lands on the wrong side of a border, a whole step of
+// its code.)
+__device__ __forceinline__ float cut_odd(double v) {
+    return __uint_as_float(__float_as_uint(__double2float_rz(v)) | ((__double2loint(v) & 0x1fffffff) != 0));
+}
+// How a row's pair of values is turned: in 64 bits, cut as above (kv_format 5),
+struct TurnOdd {
+    const uint64_t* step;
+    long long pos;
+    double m;
+    __device__ __forceinline__ float2 operator()(int pair, float a, float b) const {
+        const double2 cs = rope_turn_f64(step[pair], pos, m);
+        const double x = a, y = b;
+        return make_float2(cut_odd(x * cs.x - y * cs.y), cut_odd(x * cs.y + y * cs.x));
+    }
+};
+// or as ds4sp_rope does, with the row's cos and sin at hand.
+struct TurnBy {
+    const float2* cs;
+    __device__ __forceinline__ float2 operator()(int pair, float a, float b) const {
+        return make_float2(a * cs[pair].x - b * cs[pair].y, a * cs[pair].y + b * cs[pair].x);
+    }
+};
+
+struct TurnNot {};                              // no row is turned (p.rotate is 0)
+
 // A rotated chunk c of row i, loaded as `a`, in fp32 (p.fast).
-template <class T>
-__device__ __forceinline__ void turn_eight(const CacheRows& p, const RopeTable& tab, const uint64_t* step, int i,
+template <class T, class Turn>
+__device__ __forceinline__ void turn_eight(const CacheRows& p, const RopeTable& tab, const Turn& turn, int i,
                                            int c, const Eight<T>& a, float (&v)[8]) {
-    const long long pos = position_of(p, i);
     const int r0 = 8 * c - tab.offset, half = tab.dims / 2;
     if (tab.half_layout) {
         const bool upper = r0 >= half;
         const Eight<T> b = load_eight(static_cast<const T*>(p.x) + i * p.x_ld + 8 * c + (upper ? -half : half));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float2 cs = rope_turn(step[(upper ? r0 - half : r0) + k], pos, tab.m);
             const float s = to_f32(a.e[k]), o = to_f32(b.e[k]);
-            v[k] = upper ? o * cs.y + s * cs.x : s * cs.x - o * cs.y;
+            const float2 t = turn((upper ? r0 - half : r0) + k, upper ? o : s, upper ? s : o);
+            v[k] = upper ? t.y : t.x;
         }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float2 cs = rope_turn(step[r0 / 2 + k], pos, tab.m);
-            const float a0 = to_f32(a.e[2 * k]), b0 = to_f32(a.e[2 * k + 1]);
-            v[2 * k] = a0 * cs.x - b0 * cs.y;
-            v[2 * k + 1] = a0 * cs.y + b0 * cs.x;
+            const float2 t = turn(r0 / 2 + k, to_f32(a.e[2 * k]), to_f32(a.e[2 * k + 1]));
+            v[2 * k] = t.x;
+            v[2 * k + 1] = t.y;
         }
     }
 }
 
 // Eight values of row i (of the n written) at dims 8c .. 8c+7, rotated, in fp32.
-template <class T>
-__device__ __forceinline__ void load_chunk(const CacheRows& p, const RopeTable& tab, const uint64_t* step,
+template <class T, class Turn>
+__device__ __forceinline__ void load_chunk(const CacheRows& p, const RopeTable& tab, const Turn& turn,
                                            int i, int c, float (&v)[8]) {
+    constexpr bool kTurns = !std::is_same<Turn, TurnNot>::value;
     const T* row = static_cast<const T*>(p.x) + i * p.x_ld;
     const int d0 = 8 * c;
     if (p.fast) {
         const Eight<T> a = load_eight(row + d0);
-        if (turned(p, tab, c)) {
-            turn_eight<T>(p, tab, step, i, c, a, v);
-        } else {
+        if constexpr (kTurns)
+            if (turned(p, tab, c)) {
+                turn_eight<T>(p, tab, turn, i, c, a, v);
+                return;
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = to_f32(a.e[k]);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = to_f32(a.e[k]);
         return;
     }
-    const long long pos = p.rotate ? position_of(p, i) : 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int d = d0 + k, r = d - tab.offset, half = tab.dims / 2;
         v[k] = to_f32(row[d]);
-        if (!p.rotate || r < 0 || r >= tab.dims) continue;
-        const bool second = tab.half_layout ? r >= half : r & 1;
-        const int pair = tab.half_layout ? (second ? r - half : r) : r / 2;
-        const int od = tab.half_layout ? (second ? d - half : d + half) : (second ? d - 1 : d + 1);
-        const float2 cs = rope_turn(step[pair], pos, tab.m);
-        const float o = to_f32(row[od]);
-        v[k] = second ? o * cs.y + v[k] * cs.x : v[k] * cs.x - o * cs.y;
+        if constexpr (kTurns) {
+            if (!p.rotate || r < 0 || r >= tab.dims) continue;
+            const bool second = tab.half_layout ? r >= half : r & 1;
+            const int pair = tab.half_layout ? (second ? r - half : r) : r / 2;
+            const int od = tab.half_layout ? (second ? d - half : d + half) : (second ? d - 1 : d + 1);
+            const float o = to_f32(row[od]);
+            const float2 t = turn(pair, second ? o : v[k], second ? v[k] : o);
+            v[k] = second ? t.y : t.x;
+        }
     }
 }
 
@@ -166,21 +197,36 @@ __device__ __forceinline__ uint2 q4_codes(const float (&v)[8], float d) {
     return make_uint2(w[0], w[1]);
 }
 
+constexpr int kWriteTurns = 1280;               // (256 / 32 + 2) rows of 128 pairs; other widths have fewer
+
 // Four lanes per block of 32 values, eight values each: the block's largest magnitude (and
 // for Q4_0 its first extreme) over the four by shuffles, the codes as in quantize_rows_kernel.
 // Rows are stored at out + row * row_bytes. FMT: kFmtF16, kFmtQ8, kFmtQ4 or kFmtQ8Q4.
-template <class T, int FMT>
+// TURNED: whether rows are rotated. Measured, 122,880 fp16 rows of 576, without a rotation and with
+// 64 rotary dims: fp16 rows 49 and 80 us, Q8_0 102 and 143, Q4_0 103 and 148, Q8 K / Q4 V 166 and
+// 213 (the last is 254 MB, 39 us at the copy rate: the quotients bound it, not memory).
+template <class T, int FMT, bool TURNED>
 __global__ void __launch_bounds__(256)
 cache_write_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab, uint8_t* __restrict__ out,
                    int row_bytes) {
-    __shared__ uint64_t step[kRopeMaxDims / 2];
-    load_steps(tab, p.rotate, step);
     const int chunks = p.dims / 8;
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
     const bool in = id < (long long)p.n * chunks;
     const int i = in ? (int)(id / chunks) : 0, c = in ? (int)(id % chunks) : 0;
     float v[8];
-    load_chunk<T>(p, tab, step, i, c, v);
+    if constexpr (TURNED) {
+        // The turns of the block's rows, from `first` on (at most 256 / chunks + 2 of them, of
+        // min(4 chunks, 128) pairs), a thread one at a time.
+        __shared__ float2 turns[kWriteTurns];
+        const int first = (int)((long long)blockIdx.x * 256 / chunks), pairs = tab.dims / 2;
+        const int rows = min((int)(((long long)blockIdx.x * 256 + 255) / chunks) + 1, p.n) - first;
+        for (int k = threadIdx.x; k < rows * pairs; k += 256)
+            turns[k] = rope_turn(tab.step[k % pairs], position_of(p, first + k / pairs), tab.m);
+        __syncthreads();
+        load_chunk<T>(p, tab, TurnBy{turns + (in ? i - first : 0) * pairs}, i, c, v);
+    } else {
+        load_chunk<T>(p, tab, TurnNot{}, i, c, v);
+    }
     uint8_t* row = out + (long long)(p.row0 + i) * row_bytes;
     if constexpr (FMT == kFmtF16) {
         if (!in) return;
@@ -326,14 +372,17 @@ __device__ __forceinline__ uint2 codes_of(const Eight<T>& a, unsigned long long 
 // eighth chunk of eight values. HELD (up to 576 dims, aligned): the unrotated values as they
 // were loaded stay in registers between the block's maximum and the rounding, all loads in
 // flight at once (16-bit values: 64 registers, two CTAs an SM, so that one block's loads run
-// under the other's arithmetic), and of a rotated part of up to 64 dims the one chunk that a
-// lane has, turned once. What is not held is a loop of its own and computed twice (a rotated
-// part of 64 dims that way: 5 us more below). Measured, 122,880 bf16 rows of 576 with 64 rotary
-// dims: 213 MB in 46.0 us (4.6 TB/s, 0.72 of the copy rate), bound by the blocks' two phases and
-// by instructions (issue 59% busy, the integer pipe 55%: each value is unpacked, scaled and
-// converted in fp32). A CTA that goes on to another block, loading it as it stores this one's
-// chunks, spills: 78 us; the next block prefetched to L2: the same time.
-template <class T, bool HELD>
+// under the other's arithmetic), and of a rotated part of up to 64 dims (kTurnedOnce) the one
+// chunk that a lane has, turned once. What is not held is a loop of its own and computed twice
+// (kTurnedTwice). The three are kernels of their own: in one, the loops' registers were spilled in
+// all (45.1 us below, 43.7 without a rotation). Measured, 122,880 bf16 rows of 576 with 64 rotary
+// dims: 213 MB in 36.9 us (5.8 TB/s, 0.90 of the copy rate; halves 45.6), 34.7 us without a
+// rotation, 80 us with 128 rotary dims; 61,440 fp32 rows (one CTA an SM) in 38.8 us. Turned in fp32
+// the last two took 68 and 34.3: 64 bits cost most where they are computed twice, or where no
+// other CTA's loads run under them. A CTA that goes on to another block, loading it as it stores
+// this one's chunks, spills; the next block prefetched to L2: the same time.
+enum HowTurned { kNotTurned, kTurnedOnce, kTurnedTwice };
+template <class T, bool HELD, HowTurned TURNED>
 __global__ void __launch_bounds__(kE4M3Threads, sizeof(T) == 2 ? 2 : 1)
 cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_constant__ RopeTable tab,
                         uint8_t* __restrict__ cache) {
@@ -348,10 +397,11 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
     float* record = reinterpret_cast<float*>(base + kScaleBlock * p.dims);
     const int old = blockIdx.x == 0 ? p.row0 % kScaleBlock : 0;   // rows kept from before
     // HELD: the chunks of steps in `held` are in registers; rotated ones are [rot0, rot1), at most
-    // one a lane where `one`: it is turned once, while the others' loads are on their way.
-    const int rot0 = p.rotate ? tab.offset / 8 : 0, rot1 = p.rotate ? rot0 + tab.dims / 8 : 0;
-    const bool one = HELD && rot1 - rot0 <= 8, mine = one && in && l < rot1 - rot0;
-    const int loop0 = HELD ? rot0 : 0, loop1 = HELD ? (one ? rot0 : rot1) : chunks;
+    // one a lane where kTurnedOnce: it is turned while the others' loads are on their way.
+    const int rot0 = TURNED ? tab.offset / 8 : 0, rot1 = TURNED ? rot0 + tab.dims / 8 : 0;
+    constexpr bool one = HELD && TURNED == kTurnedOnce;
+    const bool mine = one && in && l < rot1 - rot0;
+    const int loop0 = HELD ? rot0 : 0, loop1 = HELD ? (TURNED == kTurnedTwice ? rot1 : rot0) : chunks;
     Eight<T> v[HELD ? kE4M3Held : 1], turn;
     uint32_t held = 0;
     if constexpr (HELD)
@@ -365,25 +415,21 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
                     v[s] = load_eight(row + 64 * s);
                 }
             }
-            if (mine) turn = load_eight(row + 8 * rot0);
+            if (one && mine) turn = load_eight(row + 8 * rot0);
         }
     const float old_scale = old ? *record : 0.f;
     load_steps(tab, p.rotate, step);
 
     float top = 0.f, turned_to[8];
-    if constexpr (HELD)
-        if (mine) {
-            turn_eight<T>(p, tab, step, i, rot0 + l, turn, turned_to);
-            top = top_of(turned_to, top);
-        }
     if (in) {
         // (without HELD every chunk goes this way)
+        if constexpr (!HELD || TURNED == kTurnedTwice)
 #pragma unroll 1
-        for (int c = loop0 + l; c < loop1; c += 8) {
-            float u[8];
-            load_chunk<T>(p, tab, step, i, c, u);
-            top = top_of(u, top);
-        }
+            for (int c = loop0 + l; c < loop1; c += 8) {
+                float u[8];
+                load_chunk<T>(p, tab, TurnOdd{step, p.rotate ? position_of(p, i) : 0, tab.m}, i, c, u);
+                top = top_of(u, top);
+            }
         if constexpr (HELD) {
             using Two = typename Packed<T>::type;
             Two two;
@@ -401,6 +447,11 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
             }
         }
     }
+    if constexpr (one)
+        if (mine) {
+            turn_eight<T>(p, tab, TurnOdd{step, position_of(p, i), tab.m}, i, rot0 + l, turn, turned_to);
+            top = top_of(turned_to, top);
+        }
     // (a float that is not negative orders as its bits do)
     const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     if (tid % 32 == 0) warp_top[tid / 32] = most;
@@ -436,14 +487,15 @@ cache_write_e4m3_kernel(const __grid_constant__ CacheRows p, const __grid_consta
 #pragma unroll
         for (int s = 0; s < kE4M3Held; ++s)
             if (held >> s & 1u) *reinterpret_cast<uint2*>(to + 64 * s) = codes_of<T>(v[s], inv2);
-    if constexpr (HELD)
+    if constexpr (one)
         if (mine) *reinterpret_cast<uint2*>(to + 8 * rot0) = codes_of(turned_to, inv2);
+    if constexpr (!HELD || TURNED == kTurnedTwice)
 #pragma unroll 1
-    for (int c = loop0 + l; c < loop1; c += 8) {
-        float u[8];
-        load_chunk<T>(p, tab, step, i, c, u);
-        *reinterpret_cast<uint2*>(base + (long long)r * p.dims + 8 * c) = codes_of(u, inv2);
-    }
+        for (int c = loop0 + l; c < loop1; c += 8) {
+            float u[8];
+            load_chunk<T>(p, tab, TurnOdd{step, p.rotate ? position_of(p, i) : 0, tab.m}, i, c, u);
+            *reinterpret_cast<uint2*>(base + (long long)r * p.dims + 8 * c) = codes_of(u, inv2);
+        }
 }
 
 // ---------------------------------------------------------------- reading back
