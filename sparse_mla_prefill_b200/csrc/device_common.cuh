@@ -104,12 +104,17 @@ __device__ __forceinline__ void give_up(const WaitCtl& w) {
     if (w.abort_word) *reinterpret_cast<volatile uint32_t*>(w.abort_word) = w.epoch;
 }
 
-// What a role that gave up does last, before its CTA ends: arrivals of copies and of commits
+// What a role does last, before its CTA ends. After a give-up, arrivals of copies and of commits
 // have no wait of their own where nobody waits for their phase any more, so the CTA, whose
-// shared memory they write, stays for 50 us (bounded by the clock alone).
-__device__ __forceinline__ void linger() {
-    const unsigned long long t0 = global_ns();
-    while (global_ns() - t0 < 50000ull) __nanosleep(1000);
+// shared memory they write, stays for 50 us (bounded by the clock alone). Every lane of the warp
+// calls it: a single lane may have given up, and the warp is whole again afterwards, as the block
+// barrier and the TMEM release that follow need it.
+__device__ __forceinline__ void linger_if(bool abort) {
+    if (abort) {
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 50000ull) __nanosleep(1000);
+    }
+    __syncwarp();
 }
 
 // Wait for the phase of the given parity to complete. Gives up (returns false, records

@@ -402,7 +402,7 @@ indexer_tcgen05_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
     }
 
-    if (abort) linger();
+    linger_if(abort);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -408,7 +408,7 @@ indexer_topk_fused_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
     }
 
-    if (abort) linger();
+    linger_if(abort);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(attn::Roles<KVF>::THREADS, 1) sparse_attn_mma_
         // after a give-up no consumer has waited for them.
         cp_async_commit();
         cp_async_wait<0>();
-        if (abort) linger();
+        linger_if(abort);
     } else {
         // ================================================================ consumers
         regs_increase<R::CREGS>();

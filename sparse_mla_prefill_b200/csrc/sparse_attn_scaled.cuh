@@ -834,10 +834,8 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
         }
     }
 
-    if (abort) {
-        give_up(p.wc);
-        linger();
-    }
+    if (abort) give_up(p.wc);
+    linger_if(abort);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(tcattn::THREADS, 1) sparse_attn_tc_kernel(Attn
         }
     }
 
-    if (abort) linger();
+    linger_if(abort);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
