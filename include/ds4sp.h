@@ -98,7 +98,10 @@ typedef struct {
                             -- at 64 indexer heads) in a call of at most 1,024 token
                             blocks; otherwise the two kernels run. Indices are
                             the same bits either way; 1 is the faster prefill and
-                            the Python binding's default. Other values are
+                            the Python binding's default. A pipeline wait that gives up
+                            (one second, see ds4sp_debug_set_wait_limit_ns) is reported
+                            by the status word in form 0; in form 1 it may end in a
+                            launch failure instead. Other values are
                             DS4SP_ERR_INVALID_ARG */
     int kv_format;       /* storage of kv_raw and kv_cmp: 0 = fp16 rows of 576 values
                             (1152 bytes); 1 = Q8_0 and 2 = Q4_0 quantized rows (one row
@@ -282,8 +285,12 @@ ds4sp_status ds4sp_debug_fail_launches(ds4sp_handle* h, int n);
  * shorten the waits of later launches.
  *   ns  the limit for this handle's later launches, in nanoseconds; 0 = give up at the
  *       first wait that is not already complete; negative = back to the default.
- * Below the default the indexer and the top-k run as two kernels whatever topk_mode says:
- * the fused kernel's give-up is not provoked. */
+ * The fused kernel of topk_mode 1 is an exception: with the limit at 0, three of eleven
+ * prefills by it ended in a launch failure (which ends the CUDA context) instead of a status
+ * bit, and the cause is not known. Its own second's wait has never been seen to run out; a
+ * caller who has to rely on the status bit even then takes topk_mode 0. Below the default limit
+ * the indexer and the top-k run as two kernels whatever topk_mode says, so this call does not
+ * reach the fused kernel's give-up, which is untested. */
 ds4sp_status ds4sp_debug_set_wait_limit_ns(ds4sp_handle* h, long long ns);
 
 /* Explicit-mask visibility, a debug form of the path for the "explicit-mask versus

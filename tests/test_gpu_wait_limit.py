@@ -3,11 +3,15 @@
 Every pipeline wait inside the kernels has a limit (about one second by default). A
 test cannot make a healthy pipeline stall, so it lowers the limit instead:
 ds4sp_debug_set_wait_limit_ns(h, 0) makes every wait give up at its first miss. The
-2048-token band then runs with waits that give up, in both top-k forms (the fused
-indexer + top-k kernel and the two-kernel form): the calls must return, the kernels
-must end (the test would hang otherwise), the status word must carry bit 1 (a wait gave
-up), and once the default limit is back the next prefill must give the same bits as
-the one before, which is itself checked against the oracle on a sample of tokens.
+2048-token band then runs with waits that give up, by handles of both top-k modes: the
+calls must return, the kernels must end (the test would hang otherwise), the status word
+must carry bit 1 (a wait gave up), and once the default limit is back the next prefill must
+give the same bits as the one before, which is itself checked against the oracle on a
+sample of tokens.
+
+Under a lowered limit both modes run the indexer and the top-k as two kernels
+(test_gpu_wait_limit_form.py): the second case is that fallback and the return to the fused
+indexer + top-k kernel, whose own give-up is not tested.
 """
 import numpy as np
 import pytest
