@@ -344,6 +344,10 @@ def ds4sp_quantize_kv(x, kv_format: int, out=None, stream=None):
         out = torch.empty(max(ds4sp_cache_bytes(5, dims, rows), 16), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((rows, max(rb, 16)), dtype=torch.uint8, device=x.device)
+    need = ds4sp_cache_bytes(5, dims, rows) if kv_format == 5 else rows * rb
+    if out.numel() * out.element_size() < need:
+        raise Ds4spError(ERR_INVALID_ARG, "out", f"{out.numel() * out.element_size()} bytes, {rows} rows of "
+                         f"kv_format {kv_format} need {need}")
     _check(load_library().ds4sp_quantize_kv(_ptr(x, "x", torch.float16), rows, dims, kv_format,
                                             _ptr(out, "out", torch.uint8), _stream(stream)),
            "ds4sp_quantize_kv")

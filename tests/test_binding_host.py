@@ -1,0 +1,28 @@
+"""What the Python binding refuses before it calls the library: every call here has host tensors
+or none that is read, and must be refused with the message of its own check."""
+import pytest
+import torch
+
+from sparse_mla_prefill_b200 import build as B
+from sparse_mla_prefill_b200 import ds4sp as D
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    B.build()
+    D.load_library()
+
+
+def refused(match):
+    return pytest.raises(D.Ds4spError, match=match)
+
+
+@pytest.mark.parametrize("fmt,rows,dims", [(1, 3, 576), (2, 1, 64), (3, 5, 576), (5, 1, 576), (5, 65, 64)])
+def test_quantizer_refuses_an_output_that_is_too_small(fmt, rows, dims):
+    need = D.ds4sp_cache_bytes(fmt, dims, rows)
+    x = torch.zeros(rows, dims, dtype=torch.float16)
+    for size in (0, 16, need - 1):
+        with refused(f"need {need}"):
+            D.ds4sp_quantize_kv(x, fmt, out=torch.zeros(size, dtype=torch.uint8))
+    with refused("CUDA device"):                      # large enough: the next check's refusal
+        D.ds4sp_quantize_kv(x, fmt, out=torch.zeros(need, dtype=torch.uint8))
