@@ -378,10 +378,22 @@ def _stream_on(dev: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+_I32_MAX = (1 << 31) - 1
+
+
+def _int32(v: int, name: str) -> None:
+    # (ctypes would keep a larger one's low 32 bits: row 2^32 would be written as row 0)
+    if not 0 <= v <= _I32_MAX:
+        raise Ds4spError(ERR_INVALID_ARG, name, f"{v}, expected 0 .. {_I32_MAX}")
+
+
 def _rows(t: torch.Tensor, name: str, dims: int, dev: int) -> int:
     """The dtype code of a strided tensor of `dims` dimensions whose last one is contiguous, on
     the current device, whose stream the call uses."""
     code = _DTYPES.get(t.dtype)
+    if t.numel() > _I32_MAX:
+        for v in t.shape:
+            _int32(v, name)
     if t.get_device() != dev or t.dim() != dims or code is None or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise Ds4spError(ERR_INVALID_ARG, name, f"expected a float16, bfloat16 or float32 tensor of {dims} "
                          "dimensions, the last one contiguous, on the current CUDA device; got "
@@ -404,8 +416,8 @@ def ds4sp_rope(x, rope: ds4sp_rope_config, out=None, positions=None, pos0: int =
     x itself for in place). positions: int32 [n_tokens], or None for pos0 + i * pos_step.
     transpose: the transposed rotation, the gradient with respect to x."""
     dev = _device()
-    code = _rows(x, "x", 3, dev)
     shape = x.shape
+    code = _rows(x, "x", 3, dev)
     n, heads, head = shape
     if out is None:
         out = x.new_empty(shape)
@@ -440,7 +452,7 @@ def _cache(cache: torch.Tensor, kv_format: int, dims: int, dev: int) -> int:
     unit, size = _cache_unit(kv_format, dims)
     if size == 0:
         raise Ds4spError(ERR_INVALID_ARG, "cache", f"kv_format {kv_format} with rows of {dims} values")
-    return cache.numel() * cache.element_size() // size * unit
+    return min(cache.numel() * cache.element_size() // size * unit, _I32_MAX)
 
 
 def ds4sp_cache_write(cache, kv_format: int, x, row0: int, rope: Optional[ds4sp_rope_config] = None,
@@ -449,6 +461,7 @@ def ds4sp_cache_write(cache, kv_format: int, x, row0: int, rope: Optional[ds4sp_
     of ``cache`` (uint8, ds4sp_cache_bytes(kv_format, dims, rows) bytes; float16 rows for
     kv_format 0), after turning part of each (rope)."""
     dev = _device()
+    _int32(row0, "row0")
     code = _rows(x, "x", 2, dev)
     n, dims = x.shape
     rows = _cache(cache, kv_format, dims, dev)
@@ -462,9 +475,13 @@ def ds4sp_cache_read(cache, kv_format: int, dims: int, rows=None, row0: int = 0,
     """Rows ``rows`` (int32) or row0 .. row0+n-1 of ``cache`` as values: returns ``out``
     ([n, dims], or [n, 512] for part 1, the value; allocated as ``dtype`` if None)."""
     dev = _device()
+    _int32(row0, "row0")
+    if n is not None:
+        _int32(n, "n")
     held = _cache(cache, kv_format, dims, dev)
     if n is None:
         n = held - row0 if rows is None else rows.numel()
+        _int32(n, "rows")
     width = 512 if part == 1 else dims
     if out is None:
         if dtype not in _DTYPES:

@@ -26,3 +26,24 @@ def test_quantizer_refuses_an_output_that_is_too_small(fmt, rows, dims):
             D.ds4sp_quantize_kv(x, fmt, out=torch.zeros(size, dtype=torch.uint8))
     with refused("CUDA device"):                      # large enough: the next check's refusal
         D.ds4sp_quantize_kv(x, fmt, out=torch.zeros(need, dtype=torch.uint8))
+
+
+BIG = 1 << 32
+
+
+def test_sizes_and_rows_beyond_32_bits_are_refused():
+    """The library counts rows in 32 bits; a larger count would reach it cut to its low bits."""
+    cache, x = torch.zeros(65 * 576, dtype=torch.uint8), torch.zeros(1, 576)
+    for row0 in (BIG, BIG + 3, 1 << 31, -1, -BIG):
+        with refused("^row0:"):
+            D.ds4sp_cache_write(cache, 5, x, row0)
+        with refused("^row0:"):
+            D.ds4sp_cache_read(cache, 5, 576, row0=row0, n=1)
+    for n in (BIG + 1, -1):
+        with refused("^n:"):
+            D.ds4sp_cache_read(cache, 5, 576, n=n)
+    with refused(f"^x: {BIG + 1}"):
+        D.ds4sp_cache_write(cache, 5, x.expand(BIG + 1, 576), 0)
+    for shape in ((BIG + 1, 1, 64), (1, BIG + 1, 64), (1 << 31, 1, 64)):
+        with refused(f"^x: {max(shape)}"):
+            D.ds4sp_rope(torch.zeros(1, 1, 64).expand(shape), D.make_rope(64))
