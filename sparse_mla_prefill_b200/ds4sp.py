@@ -387,6 +387,12 @@ def _int32(v: int, name: str) -> None:
         raise Ds4spError(ERR_INVALID_ARG, name, f"{v}, expected 0 .. {_I32_MAX}")
 
 
+def _no_graph(name: str) -> None:
+    if torch.is_grad_enabled():
+        raise Ds4spError(ERR_INVALID_ARG, name, "requires a gradient, which the result would be cut off from: call "
+                         "under torch.no_grad() or on the detached tensor (transpose=True turns the gradient)")
+
+
 def _rows(t: torch.Tensor, name: str, dims: int, dev: int) -> int:
     """The dtype code of a strided tensor of `dims` dimensions whose last one is contiguous, on
     the current device, whose stream the call uses."""
@@ -414,7 +420,10 @@ def ds4sp_rope(x, rope: ds4sp_rope_config, out=None, positions=None, pos0: int =
     """Turn the rotary part of x [n_tokens, heads, head_dim] (float16, bfloat16 or float32;
     any token and head strides) and return ``out`` (of x's shape and type, allocated if None;
     x itself for in place). positions: int32 [n_tokens], or None for pos0 + i * pos_step.
-    transpose: the transposed rotation, the gradient with respect to x."""
+    transpose: the transposed rotation, the gradient with respect to x. The result is not part
+    of torch's graph: a tensor that requires a gradient is refused while gradients are enabled."""
+    if x.requires_grad or (out is not None and out.requires_grad):
+        _no_graph("x" if x.requires_grad else "out")
     dev = _device()
     shape = x.shape
     code = _rows(x, "x", 3, dev)

@@ -47,3 +47,16 @@ def test_sizes_and_rows_beyond_32_bits_are_refused():
     for shape in ((BIG + 1, 1, 64), (1, BIG + 1, 64), (1 << 31, 1, 64)):
         with refused(f"^x: {max(shape)}"):
             D.ds4sp_rope(torch.zeros(1, 1, 64).expand(shape), D.make_rope(64))
+
+
+def test_rope_refuses_a_tensor_it_would_cut_off_from_its_gradient():
+    x, plain, rope = torch.zeros(1, 1, 64, requires_grad=True), torch.zeros(1, 1, 64), D.make_rope(64)
+    with refused("^x: requires a gradient"):
+        D.ds4sp_rope(x, rope)
+    with refused("^x: requires a gradient"):
+        D.ds4sp_rope(2 * x, rope, out=plain)
+    with refused("^out: requires a gradient"):
+        D.ds4sp_rope(plain, rope, out=x)
+    for call in (lambda: D.ds4sp_rope(x.detach(), rope), lambda: torch.no_grad()(D.ds4sp_rope)(x, rope)):
+        with refused("CUDA device"):                  # the next check's refusal
+            call()
