@@ -86,6 +86,7 @@ typedef struct {
                             lo = fp16(p - hi)), about 22 significant bits, at twice the
                             P . V tensor work ("FP32-staged streaming MLA" of "perf(ds4):
                             unify gfx1151 sparse-prefill stack", Validation completed);
+                            kv_format 5 has its own terms, see there;
                             other values are DS4SP_ERR_INVALID_ARG */
     int topk_mode;       /* steps 1-2: 0 = the indexer writes fp32 scores to the caller's
                             workspace and a top-k kernel reads them back; 1 = one fused
@@ -118,8 +119,14 @@ typedef struct {
                             stores them (ds4sp_cache_bytes(5, 576, rows) bytes): the
                             attention multiplies the e4m3 codes as they are, on the
                             tcgen05 tensor cores, with the queries and the probabilities
-                            as sums of e4m3 terms (pv_mode 0: three terms, fp16
-                            probabilities; 1: five, about 20 bits); it needs exp_mode 0 and attn_kernel
+                            as sums of e4m3 terms. A row's weight is p * s (s its
+                            block's scale): pv_mode 0 holds it to 11 bits (three
+                            terms), 1 to about 20 (five), but to no less than 2^-16
+                            or 2^-23 of the largest weight of the token's rows, so
+                            where blocks' scales differ by 2^10 or more, the rows of
+                            the small ones lose bits of their probability (one row of
+                            scale 2^10 times the others': 1e-3 or 3e-5 of sum p |v|,
+                            2^12 times: 4e-3 or 7e-5). It needs exp_mode 0 and attn_kernel
                             0. Other values are DS4SP_ERR_INVALID_ARG
                             ("Q4_0 K/V cache" and "Q8 K / Q4 V", "perf(ds4): extend sparse
                             prefill scheduling to 10K", Production workflow and the
