@@ -122,12 +122,12 @@ typedef struct {
                             as sums of e4m3 terms. A row's weight is p * s (s its
                             block's scale): pv_mode 0 holds it to 11 bits (three
                             terms), 1 to about 20 (five), but to no less than 2^-16
-                            or 2^-23 of the largest weight of the token's rows, so
-                            where blocks' scales differ by 2^10 or more, the rows of
+                            or 2^-25 of the largest weight of the token's rows, so
+                            where blocks' scales differ by 2^8 or more, the rows of
                             the small ones lose bits of their probability (one row of
-                            scale 2^10 times the others': 1e-3 or 3e-5 of sum p |v|,
-                            2^12 times: 4e-3 or 7e-5). It needs exp_mode 0 and attn_kernel
-                            0. Other values are DS4SP_ERR_INVALID_ARG
+                            scale 2^10 times the others': 1e-3 or 7e-6 of sum p |v|,
+                            2^12 times: 4e-3 or 3e-5; not in calls of a few tokens).
+                            It needs exp_mode 0 and attn_kernel 0. Other values are DS4SP_ERR_INVALID_ARG
                             ("Q4_0 K/V cache" and "Q8 K / Q4 V", "perf(ds4): extend sparse
                             prefill scheduling to 10K", Production workflow and the
                             clean-head validation; the pages name the formats without

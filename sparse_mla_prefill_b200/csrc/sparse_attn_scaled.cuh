@@ -15,25 +15,28 @@
 //   O^T = codes^T . [b0 .. b_{NT-1}]         M = 128 value dims x 4, N = NT x 16, K = rows
 //   out = O / sum(w / s_r)
 //
-// NT = 3 terms hold the weight's fp16 rounding (pv_mode 0: fp16 probabilities), five the weight
-// to 2^-20, and to 2^-28 of a weight of 1 where it is small (pv_mode 1: the result is right to
-// fp32 sums; four terms would leave small weights 2^-23, 3e-6 of the result). Each rounding to
+// NT = 3 terms hold the weight's fp16 rounding (pv_mode 0), five the weight to 2^-20, and to
+// 2^-28 of a weight of 1 where it is small (pv_mode 1: the result is as right as fp32 sums; four
+// terms would leave small weights 2^-23, 3e-6 of the result). Each rounding to
 // e4m3 is of what the terms before it left, so nothing is lost but the last one's remainder.
 // Products of e4m3 values are exact in the fp32 accumulator.
 //
 // The last term's spacing is fixed, so a weight p s is held to no less than 2^-16 (three terms) or
-// 2^-23 (five) of the token's largest: a row of a block of small scale beside one whose scale is
-// 2^r times larger loses about r bits of its probability beyond the first four (measured, r = 10:
-// 1e-3 or 2.7e-5 of sum p |v|; 2^-16 and 2^-23 are bounds, rows' errors have either sign).
+// 2^-25 (five) of the token's largest: a row of a block of small scale beside one whose scale is
+// 2^r times larger loses about r - 4 bits of its probability (measured, r = 10: 1e-3 or 7e-6 of
+// sum p |v|; 2^-16 and 2^-25 are bounds, rows' errors have either sign). A unit that is its item's
+// only one, as all are in the few-token form, keeps ten bits more.
 //
 // What bounds it: shared memory, and the instructions around it. Each unit's rows pass through
 // the tensor cores twice, from shared memory: an M = 128, K = 32 instruction takes what its
 // operands take at 128 bytes a cycle (measured: 45 cycles for S, 53 for O^T, mostly the 4 KB of
 // A), so 128 rows take 18 + 16 of them, about 1,640 cycles, and N costs little, which is why the
 // terms are columns. The gather and the roles' own accesses add about 800. Measured, 10,240
-// tokens with 512 + 128 rows each: 565 us (pv_mode 1; each SM 3,300 cycles a unit; the softmax
-// is busy for 2,500 of them, the tensor pipe for half, shared memory for 75%), against 1,097 us
-// of the fp16 cache's kernel with fp16 probabilities, 1,290 us with fp32-staged ones.
+// tokens with 512 + 128 rows each, at 1.96 GHz: 575 us (pv_mode 1; each SM 3,500 cycles a unit;
+// the softmax is busy for most of them, the tensor pipe for half, shared memory for 70%), 538 us
+// (pv_mode 0), against 1,097 us of the fp16 cache's kernel with fp16 probabilities, 1,290 us with
+// fp32-staged ones. In calls without a pause the card reaches its power limit within 0.2 s and the
+// clock falls to 1.75 GHz: 560 us then becomes 635.
 //
 // What did not help: gathers by TMA (26 cycles for each 512 bytes), two groups of gather warps,
 // more slabs, queries in warps of their own or double-buffered, a vote whose wait runs under the
@@ -48,10 +51,12 @@
 // Roles: warps 0-7 softmax, 8-11 the queries' terms and the output, 12-15 gather (16-byte
 // cp.async), warp 16 issues S and warp 17 O^T: an MMA of this size is short
 // against a wait's latency, and with two issuers each one's waits run under the other's MMAs.
-// The reference ref_h is set above the first unit's maximum (by 2^5 with five terms), and
+// The reference ref_h is set above the maximum of the first unit that has rows (by 2^3), and
 // raised, O and the sums rescaled, only when a unit exceeds it by 2^8, e4m3 holding weights up
-// to 448: for logits of wide spread one unit in ten, against one in three with the maximum
-// itself.
+// to 448: for logits of wide spread one unit in six, against three in ten with the maximum
+// itself. (By 2^5, one in nine, a prefill took 562 us, but the largest weights were then 2^-5 and
+// the result's error 7e-7; 2.8e-7 now, an elementary fp32 form's 3.5e-7.) The only unit of an item
+// has its largest weight at 2^7: there is none to come that could exceed it.
 // Every wait is bounded; a wait that gives up sets the launch's abort word and every role
 // drains.
 #pragma once
@@ -81,7 +86,8 @@ constexpr int SOFTMAX_BAR = 1;                  // and 2: one per group
 constexpr int OUT_BAR = 3;
 constexpr float UNSET = 1e30f;                  // minus the reference while no row was attended
 constexpr float HEADROOM = 8.f;                 // log2 units a unit may exceed the reference, which is
-constexpr float start_of(int nt) { return nt == 5 ? 5.f : 3.f; }   // set so many above a unit's maximum
+constexpr float START = 3.f;                    // set so many above a unit's maximum,
+constexpr float START_ALONE = -7.f;             // or below it, for an item's only rows (weights up to 2^7)
 
 constexpr int OFF_SLAB = 0;
 constexpr int OFF_ROPE = OFF_SLAB + SLOTS * SLAB;
@@ -569,11 +575,12 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 }
                 if (named_barrier_or(group_bar, 128, abort)) break;
                 float alpha[HG], most = -INFINITY;
+                const float start = none && c.last() ? START_ALONE : START;
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
                     const float4 m4 = *reinterpret_cast<const float4*>(red + 4 * h);
                     const float mu = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                    const float up = (none ? mu > -INFINITY : mu > HEADROOM) ? mu + start_of(NT) : 0.f;
+                    const float up = (none ? mu > -INFINITY : mu > HEADROOM) ? mu + start : 0.f;
                     most = fmaxf(most, mu);
                     alpha[h] = fast_exp2(-up);
                     w[h] = -up;

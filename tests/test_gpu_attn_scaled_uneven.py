@@ -2,8 +2,9 @@
 sink) in a block whose scale is 2^r times the others'.
 
 A row's weight is p s, p its probability and s its block's scale, and the terms hold it to
-TOL of itself but to no less than FLOOR of the token's largest weight (test_gpu_attn_scaled's
-module text derives both). So where the sink is 0, an element's error relative to sum p |v| is at
+TOL of itself (test_gpu_attn_scaled's module text derives it) but to no less than FLOOR of the
+token's largest weight: half of the last term's smallest spacing, 2^-19 (three terms) or 2^-28
+(five), where the largest weight is 1/8 at least. So where the sink is 0, an element's error relative to sum p |v| is at
 most TOL + FLOOR * R, R the largest p s over the smallest: the probabilities' bits that an uneven
 cache costs. This is the bound that the header states; the tests hold it, and that error is
 as small as the format's own where R is near 1.
@@ -15,9 +16,10 @@ import torch
 from oracle import cache_ops as O
 from sparse_mla_prefill_b200 import build as B
 from sparse_mla_prefill_b200 import ds4sp as D
-from test_gpu_attn_scaled import FLOOR, TOL, Case, scales_of
+from test_gpu_attn_scaled import TOL, Case, scales_of
 
 pytestmark = pytest.mark.gpu
+FLOOR = {0: 2.0 ** -16, 1: 2.0 ** -25}
 
 
 @pytest.fixture(scope="module", autouse=True)
