@@ -988,13 +988,17 @@ void launch_rope_t(RopeParams& p, int v, dim3 grid, cudaStream_t s) {
     else launch_rope_v<T, 1>(p, grid, s);
 }
 
+// SMs of the one chip this library is built for: the calls without a handle spread small work by
+// it (a partitioned device only gets more blocks than it has SMs).
+constexpr int kSms = 148;
+
 // Tokens of a block: those whose rows its threads load at once, as long as that leaves two
 // blocks an SM (a small call spreads its tokens, where latency counts).
 ds4sp_status launch_rope(RopeParams& p, ds4sp_dtype t, int v, cudaStream_t s) {
     const int width = std::min(p.per_head, kRopeThreads);
     p.groups = kRopeThreads / width;
     const long long most = std::min<long long>((long long)rope_rows(p.tab.half_layout) * p.groups / p.heads, kRopeTurns / (p.tab.dims / 2));
-    p.tokens = (int)std::max<long long>(1, std::min<long long>(most, p.n / 296));
+    p.tokens = (int)std::max<long long>(1, std::min<long long>(most, p.n / (2 * kSms)));
     p.by_width.set((uint32_t)width);
     p.by_heads.set((uint32_t)p.heads);
     const dim3 grid((unsigned)((p.n + p.tokens - 1) / p.tokens), (unsigned)((p.per_head + width - 1) / width));
@@ -1058,7 +1062,7 @@ void launch_cache_read_t(const CacheRead& p, int fmt, unsigned grid, T* out, cud
 // an SM; a small call takes a row per block.
 void launch_cache_read(CacheRead& p, int fmt, void* out, ds4sp_dtype t, cudaStream_t s) {
     const int chunks = p.out_dims / 8;
-    p.block_rows = std::max(1, std::min(1024 / chunks, p.n / 592));
+    p.block_rows = std::max(1, std::min(1024 / chunks, p.n / (4 * kSms)));
     p.by_row.set((uint32_t)chunks);
     const unsigned grid = (unsigned)((p.n + p.block_rows - 1) / p.block_rows);
     if (t == DS4SP_F32) launch_cache_read_t(p, fmt, grid, static_cast<float*>(out), s);
