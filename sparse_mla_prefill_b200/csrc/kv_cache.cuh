@@ -1,8 +1,9 @@
 // Writing latent rows to a cache as they are produced, and reading them back.
 //
 // A row of x (fp16, bf16 or fp32) is rotated (optionally, the rotary part of the row:
-// rope.cuh's arithmetic, kept in fp32, or in 64 bits for kv_format 5) and stored in the cache's format: fp16, the block
-// formats of quant_kv.cuh, or kv_format 5, whose rows the scaled attention reads:
+// rope.cuh's arithmetic, kept in fp32, or in 64 bits for kv_format 5) and stored in the cache's
+// format: fp16, the block formats of quant_kv.cuh, or kv_format 5, whose rows the scaled
+// attention reads:
 //
 //   e4m3 codes with one scale 2^e for each block of 64 rows; value = code * 2^e.
 //   e is the smallest integer with max|x| <= 448 * 2^e over the block's finite values,
@@ -108,7 +109,6 @@ struct TurnBy {
 };
 
 struct TurnNot {};                              // no row is turned (p.rotate is 0)
-
 // A rotated chunk c of row i, loaded as `a`, in fp32 (p.fast).
 template <class T, class Turn>
 __device__ __forceinline__ void turn_eight(const CacheRows& p, const RopeTable& tab, const Turn& turn, int i,

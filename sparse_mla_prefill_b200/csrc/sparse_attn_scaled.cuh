@@ -575,7 +575,9 @@ sparse_attn_scaled_kernel(const __grid_constant__ AttnParams p, const __grid_con
                 }
                 if (named_barrier_or(group_bar, 128, abort)) break;
                 float alpha[HG], most = -INFINITY;
-                const float start = none && c.last() ? START_ALONE : START;
+                // (A single row keeps START: its reference, nearer 0 than the row's own negative
+                // logarithm, is exact there, so its weight is 1/8 and the output the row's values.)
+                const float start = none && c.last() && c.it.rows > 1 ? START_ALONE : START;
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
                     const float4 m4 = *reinterpret_cast<const float4*>(red + 4 * h);

@@ -45,3 +45,14 @@ def test_no_further_from_64_bits_than_an_elementary_fp32_form(k, n_swa):
     want = elementary(c.q.double(), rows.double(), seen)
     plain = elementary(c.q.float(), rows, seen).double()
     assert (out - want).norm() <= (plain - want).norm()
+
+
+@pytest.mark.parametrize("pv_mode", [0, 1])
+@pytest.mark.parametrize("n", [60, 4])
+def test_a_token_with_one_row_returns_it(n, pv_mode):
+    """One attended row (a window of one, nothing selected): the stored values themselves, where the
+    logit leaves the weight's logarithm negative (scales of 2^-7 to 2^-5, logits below 2)."""
+    c = Case(n, 0 if n == 4 else 1000, 0, 1, seed=40 + n, spread=0.0, pv_mode=pv_mode)
+    c.q.mul_(0.25)
+    rows = D.ds4sp_cache_read(c.raw, 5, 576, row0=c.t0, n=n, dtype=torch.float32)[:, :512]
+    assert torch.equal(c.run(), rows[:, None].expand(n, 16, 512))
