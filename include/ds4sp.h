@@ -294,7 +294,7 @@ ds4sp_status ds4sp_debug_fail_launches(ds4sp_handle* h, int n);
  *       first wait that is not already complete; negative = back to the default.
  * The fused kernel of topk_mode 1 is an exception: with the limit at 0, three of eleven
  * prefills by it ended in a launch failure (which ends the CUDA context) instead of a status
- * bit, and the cause is not known. Its own second's wait has never been seen to run out; a
+ * bit, and the cause is not known. Its waits of a second have never been seen to run out; a
  * caller who has to rely on the status bit even then takes topk_mode 0. Below the default limit
  * the indexer and the top-k run as two kernels whatever topk_mode says, so this call does not
  * reach the fused kernel's give-up, which is untested. */
