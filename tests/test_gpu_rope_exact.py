@@ -91,3 +91,26 @@ def test_stored_codes_are_the_exact_values_codes(dtype, dims, offset, layout):
     low, high = (O.e4m3_round((y + s * off) / scale) * scale for s in (-1, 1))
     assert ((got >= low) & (got <= high)).all()
     assert (got != O.e4m3_round(y / scale) * scale).sum() <= 1
+
+
+@pytest.mark.parametrize("dims,offset", [(64, 512), (128, 448), (34, 9)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_special_values_in_a_rotated_part(dtype, dims, offset):
+    """Infinities saturate at 448 scales, NaNs stay, neither moves the block's scale nor another
+    pair; values whose turned form passes fp32's largest saturate at the largest scale."""
+    x = torch.zeros(130, 576)
+    x[:, 0] = 16.0
+    x[3, offset], x[5, offset + 2], x[6, offset + 4] = float("inf"), float("nan"), -float("inf")
+    x[128, offset] = x[128, offset + 1] = 3.3e38
+    cache = torch.zeros(D.ds4sp_cache_bytes(5, 576, 130), dtype=torch.uint8, device="cuda")
+    D.ds4sp_cache_write(cache, 5, x.to(dtype).cuda(), 0, rope=D.make_rope(dims, offset), pos0=1)
+    got = D.ds4sp_cache_read(cache, 5, 576, row0=0, n=130, dtype=torch.float32).double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        y = O.rope(x.to(dtype).double().numpy()[:, None], 1 + np.arange(130), dims, offset)[:, 0]
+    first = y[:128]
+    assert np.array_equal(np.isnan(got[:128]), np.isnan(first))
+    at = np.isinf(first)
+    assert at.sum() >= 3 and np.array_equal(got[:128][at], np.sign(first[at]) * 448 * 2.0 ** -4)
+    rest = np.isfinite(first)
+    assert np.array_equal(got[:128][rest], O.e4m3_round(first[rest] * 2.0 ** 4) * 2.0 ** -4)
+    assert np.array_equal(got[128, offset:offset + 2], np.sign(y[128, offset:offset + 2]) * 448 * 2.0 ** 40)
